@@ -16,6 +16,7 @@ activations, the FP8-Block scheme).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -76,6 +77,21 @@ def lib() -> ctypes.CDLL:
         L.fp8_linear.restype = ctypes.c_int
         L.fp8_linear_workspace_size.argtypes = [I, I, I, ctypes.c_int]
         L.fp8_linear_workspace_size.restype = S
+        D, F, N = ctypes.c_double, ctypes.c_float, ctypes.c_int
+        L.fp8q_rope_frequencies.argtypes = [P, I, D, P]
+        L.fp8q_rope_frequencies.restype = N
+        L.fp8q_rope.argtypes = [P, I, I, I, I, I, P, P, I, N, F, P, I, I, P]
+        L.fp8q_rope.restype = N
+        L.fp8q_kv4_page_bytes.argtypes = [I, I, I]
+        L.fp8q_kv4_page_bytes.restype = S
+        L.fp8q_kv4_append.argtypes = [P, P, I, I, P, I, I, P, I, P, P, I, N, F, P]
+        L.fp8q_kv4_append.restype = N
+        L.fp8q_kv4_read.argtypes = [P, P, I, P, I, I, P, I, I, P]
+        L.fp8q_kv4_read.restype = N
+        L.fp8q_kv4_attention_workspace_size.argtypes = [P, I, I, I, I]
+        L.fp8q_kv4_attention_workspace_size.restype = S
+        L.fp8q_kv4_attention.argtypes = [P, P, I, I, I, I, P, I, I, P, P, I, I, F, N, I, P, I, I, P, P, S, P]
+        L.fp8q_kv4_attention.restype = N
         L.fp8q_status_string.argtypes = [ctypes.c_int]
         L.fp8q_status_string.restype = ctypes.c_char_p
         L.fp8q_device_error.argtypes = [ctypes.c_int]
@@ -362,6 +378,241 @@ def fp8_linear(Xq: torch.Tensor, x_scale: torch.Tensor, Wq: torch.Tensor, w_scal
     st = lib().fp8_linear(_ptr(Xq), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), M, N, K, int(mode),
                           _ptr(out), out.stride(0), _ptr(workspace), wbytes, _stream(Xq))
     _check(st, "fp8_linear")
+    return out
+
+
+# ------------------------------------------ rotary positions, 4-bit KV cache ---
+
+ROPE_HALF, ROPE_INTERLEAVED, ROPE_INVERSE = 0, 1, 2
+_ROPE_SCALINGS = {"linear": 1, "llama3": 2, "yarn": 3}
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("original_max_position", ctypes.c_double)]
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+def _on(t: torch.Tensor):
+    """The context in which a call for t's device runs: that device current."""
+    i = t.device.index
+    return contextlib.nullcontext() if i is None or i == torch.cuda.current_device() else torch.cuda.device(i)
+
+
+def _require_heads(t: torch.Tensor, name: str, ref: Optional[torch.Tensor] = None, shape=None) -> None:
+    """A bf16 CUDA tensor [tokens, heads, head_dim] with contiguous elements, on ref's device."""
+    if not t.is_cuda or (ref is not None and t.device != ref.device):
+        raise ValueError(f"{name} must be a CUDA tensor" + ("" if ref is None else f" on {ref.device}"))
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bf16, got {t.dtype}")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with unit stride in the last dimension")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _head_strides(t: torch.Tensor) -> Tuple[int, int]:
+    """(token, head) strides; those of dimensions of size 1 as in a contiguous tensor."""
+    T, H, D = t.shape
+    h = t.stride(1) if H > 1 else D
+    return (t.stride(0) if T > 1 else H * D), h
+
+
+def _require_list(t: torch.Tensor, name: str, dtype, numel: int, ref: torch.Tensor) -> None:
+    """A 1-D index or table operand: contiguous, of exactly numel elements, on ref's device."""
+    if not t.is_cuda or t.device != ref.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {ref.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {numel} elements")
+
+
+def fp8q_rope_frequencies(rot_dim: int, theta: float = 500000.0, scaling: Optional[dict] = None,
+                          device="cuda") -> torch.Tensor:
+    """The rot_dim / 2 rotary frequencies (fp64, radians per position) on `device`.
+    scaling: None, or a dict with "type" ("linear", "llama3" or "yarn"), "factor", and for the latter two
+    "original_max_position" and "low" / "high" (llama3: 1 / 4, yarn: 1 / 32 unless given)."""
+    s = None
+    if scaling is not None:
+        kind = scaling.get("type")
+        if kind not in _ROPE_SCALINGS:
+            raise ValueError(f"unknown rope scaling {kind!r}")
+        s = _RopeScaling(_ROPE_SCALINGS[kind], float(scaling["factor"]), float(scaling.get("low", 1.0)),
+                         float(scaling.get("high", 32.0 if kind == "yarn" else 4.0)),
+                         float(scaling.get("original_max_position", 0.0)))
+    host = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.float64)
+    st = lib().fp8q_rope_frequencies(host.data_ptr() or None, int(rot_dim), float(theta),
+                                     ctypes.byref(s) if s is not None else None)
+    _check(st, "fp8q_rope_frequencies")
+    return host.to(device)
+
+
+def fp8q_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, interleaved: bool = False,
+              inverse: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotate bf16 heads x [T, H, D] by positions [T] (int64) times freq (fp64 [rot_dim / 2], from
+    fp8q_rope_frequencies); elements from rot_dim on are copied.  `out` may be x itself."""
+    _require_heads(x, "x")
+    T, H, D = x.shape
+    _require_list(positions, "positions", torch.int64, T, x)
+    _require_list(freq, "freq", torch.float64, freq.shape[0] if freq.dim() else 0, x)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
+    elif out is not x:
+        _require_heads(out, "out", x, (T, H, D))
+    xt, xh = _head_strides(x)
+    yt, yh = _head_strides(out)
+    with _on(x):
+        st = lib().fp8q_rope(x.data_ptr(), T, H, D, xt, xh, positions.data_ptr(), freq.data_ptr(), 2 * freq.shape[0],
+                             (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0),
+                             float(mscale), out.data_ptr(), yt, yh, _stream(x))
+    _check(st, "fp8q_rope")
+    return out
+
+
+def fp8q_kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page of a KV4Cache's k_pages (or v_pages); 0 for sizes that are not supported."""
+    return int(lib().fp8q_kv4_page_bytes(page_size, kv_heads, head_dim))
+
+
+class KV4Cache:
+    """A paged KV cache of E2M1 codes with an E4M3 scale for each 16 elements (4.5 bits an element).
+
+    k_pages, v_pages: uint8 CUDA tensors [num_pages, kv_heads, page_size * 9 * head_dim / 16], contiguous (KV4Cache.empty
+    makes them).  k_scale, v_scale: the static fp32 factors of all values, amax / 2688 of a calibration set for the
+    formats' whole range."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_size: int, head_dim: int = 128,
+                 k_scale: float = 1.0, v_scale: float = 1.0):
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if not t.is_cuda or t.device != k_pages.device or t.dtype != torch.uint8:
+                raise ValueError(f"{name} must be a uint8 CUDA tensor (both on one device)")
+            if t.dim() != 3 or not t.is_contiguous() or t.shape != k_pages.shape or \
+                    t.shape[2] != page_size * (head_dim * 9 // 16):
+                raise ValueError(f"{name} must be contiguous [num_pages, kv_heads, page_size * 9 * head_dim / 16]")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.num_pages, self.kv_heads = int(k_pages.shape[0]), int(k_pages.shape[1])
+        self.page_size, self.head_dim = int(page_size), int(head_dim)
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.device = k_pages.device
+        self._struct = _CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), self.num_pages, self.page_size,
+                                    self.kv_heads, self.head_dim, self.k_scale, self.v_scale)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int = 64, head_dim: int = 128, k_scale: float = 1.0,
+              v_scale: float = 1.0, device="cuda") -> "KV4Cache":
+        """A cache of num_pages pages of page_size tokens, all zero."""
+        shape = (num_pages, kv_heads, page_size * (head_dim * 9 // 16))
+        return cls(torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.zeros(shape, dtype=torch.uint8, device=device), page_size, head_dim, k_scale, v_scale)
+
+
+def fp8q_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                    positions: Optional[torch.Tensor] = None, freq: Optional[torch.Tensor] = None,
+                    interleaved: bool = False, mscale: float = 1.0) -> None:
+    """Quantize k and v (bf16 [T, kv_heads, head_dim]) into the cache's slots ([T] int64, page * page_size + row;
+    negative: skipped), k rotated by positions * freq on the way (as it is with both None)."""
+    _require_heads(k, "k", cache.k_pages)
+    T = k.shape[0]
+    shape = (T, cache.kv_heads, cache.head_dim)
+    _require_heads(k, "k", cache.k_pages, shape)
+    _require_heads(v, "v", cache.k_pages, shape)
+    _require_list(slots, "slots", torch.int64, T, k)
+    if (positions is None) != (freq is None):
+        raise ValueError("positions and freq are given together")
+    R = 0
+    if positions is not None:
+        _require_list(positions, "positions", torch.int64, T, k)
+        _require_list(freq, "freq", torch.float64, freq.shape[0] if freq.dim() else 0, k)
+        R = 2 * freq.shape[0]
+    kt, kh = _head_strides(k)
+    vt, vh = _head_strides(v)
+    with _on(k):
+        st = lib().fp8q_kv4_append(cache._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), T,
+                                   _ptr(positions), _ptr(freq), R, ROPE_INTERLEAVED if interleaved else 0,
+                                   float(mscale), _stream(k))
+    _check(st, "fp8q_kv4_append")
+
+
+def fp8q_kv4_read(cache: KV4Cache, slots: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """The cached keys and values of slots [T] (int64) as bf16 [T, kv_heads, head_dim]; zeros for a negative slot."""
+    _require_list(slots, "slots", torch.int64, slots.shape[0] if slots.dim() else 0, cache.k_pages)
+    shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
+    if out is None:
+        out = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device),
+               torch.empty(shape, dtype=torch.bfloat16, device=cache.device))
+    k, v = out
+    _require_heads(k, "k", cache.k_pages, shape)
+    _require_heads(v, "v", cache.k_pages, shape)
+    kt, kh = _head_strides(k)
+    vt, vh = _head_strides(v)
+    with _on(k):
+        st = lib().fp8q_kv4_read(cache._ref, slots.data_ptr(), shape[0], k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                 _stream(k))
+    _check(st, "fp8q_kv4_read")
+    return k, v
+
+
+def fp8q_kv4_attention_workspace_size(cache: KV4Cache, num_seqs: int, tokens: int, q_heads: int,
+                                      max_q_len: int = 1) -> int:
+    with _on(cache.k_pages):
+        return int(lib().fp8q_kv4_attention_workspace_size(cache._ref, num_seqs, tokens, q_heads, max_q_len))
+
+
+def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tensor, kv_len: torch.Tensor,
+                       q_start: Optional[torch.Tensor] = None, max_q_len: int = 1, sm_scale: Optional[float] = None,
+                       causal: bool = True, window: int = 0, out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of new tokens over the cache, which already holds them.
+
+    q bf16 [T, q_heads, head_dim]; page_table int32 [B, max_pages]; kv_len int32 [B], tokens in the cache.
+    q_start int32 [B + 1]: sequence b's rows of q are its last q_start[b + 1] - q_start[b] tokens, at most max_q_len
+    (None: one row per sequence).  Rows behind q_start[B] are left as they were.  lse: fp32 [T, q_heads], written
+    when given.  `workspace`: a zero-filled uint8 buffer of fp8q_kv4_attention_workspace_size bytes (allocated here
+    when None; left zero).  -> out bf16 [T, q_heads, head_dim]"""
+    ref = cache.k_pages
+    _require_heads(q, "q", ref)
+    T, Hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q must have head_dim {cache.head_dim}")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != ref.device or \
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be int32 [sequences, max_pages] on the cache's device, rows contiguous")
+    B, max_pages = page_table.shape
+    _require_list(kv_len, "kv_len", torch.int32, B, ref)
+    if q_start is not None:
+        _require_list(q_start, "q_start", torch.int32, B + 1, ref)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _require_heads(out, "out", ref, (T, Hq, D))
+    if lse is not None:
+        _require_out(lse, "lse", torch.float32, (T, Hq), ref)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    L = lib()
+    with _on(ref):
+        if workspace is None:
+            need = int(L.fp8q_kv4_attention_workspace_size(cache._ref, B, T, Hq, int(max_q_len)))
+            if need > 0:
+                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+        else:                    # its size is checked by the library (FP8Q_ERR_INVALID_ARG)
+            _require_like(workspace, "workspace", torch.uint8, 0, ref)
+        qt, qh = _head_strides(q)
+        ot, oh = _head_strides(out)
+        st = L.fp8q_kv4_attention(cache._ref, q.data_ptr(), qt, qh, T, Hq, page_table.data_ptr(),
+                                  page_table.stride(0) if B > 1 else max_pages, max_pages, kv_len.data_ptr(),
+                                  _ptr(q_start), B, int(max_q_len),
+                                  float(D ** -0.5 if sm_scale is None else sm_scale), 1 if causal else 0, int(window),
+                                  out.data_ptr(), ot, oh, _ptr(lse), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel(), _stream(q))
+    _check(st, "fp8q_kv4_attention")
     return out
 
 

@@ -10,8 +10,15 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8q.so")
-SOURCES = ["fp8q.cu"]
-DEPS = ["fp8q.cu", "ptx.cuh", "quant.cuh", "gemm_prefill.cuh", "gemm_decode.cuh", "gemv_w8a16.cuh", "calib.cuh", "sched.cuh"]
+OBJ = os.path.join(HERE, "_build")
+SOURCES = ["fp8q.cu", "kv4.cu"]
+# What each source file is made of; the public header belongs to both.
+PARTS = {
+    "fp8q.cu": ["fp8q.cu", "ptx.cuh", "quant.cuh", "gemm_prefill.cuh", "gemm_decode.cuh", "gemv_w8a16.cuh",
+                "calib.cuh", "sched.cuh", "host.cuh"],
+    "kv4.cu": ["kv4.cu", "ptx.cuh", "rope.cuh", "kv4.cuh", "kv4_attention.cuh", "sched.cuh", "host.cuh"],
+}
+DEPS = sorted({d for parts in PARTS.values() for d in parts})
 
 
 def nvcc() -> str:
@@ -30,12 +37,16 @@ def flags(verbose: bool = False) -> list:
     return f
 
 
-def stale(lib: str = LIB) -> bool:
-    if not os.path.exists(lib):
+def _older(out: str, deps: list) -> bool:
+    if not os.path.exists(out):
         return True
-    t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", "fp8q.h")]
+    t = os.path.getmtime(out)
+    deps = [os.path.join(CSRC, d) for d in deps] + [os.path.join(ROOT, "include", "fp8q.h")]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def stale(lib: str = LIB) -> bool:
+    return _older(lib, DEPS)
 
 
 # Test build for the failure-detection tests: waits give up after 2 ms instead
@@ -48,12 +59,31 @@ TEST_FLAGS = ["-DFP8Q_TEST_HOOKS", "-DFP8Q_WAIT_LIMIT_NS=2000000ull"]
 def _compile(out: str, extra: list, force: bool, verbose: bool) -> str:
     if not force and not stale(out):
         return out
-    cmd = [nvcc()] + flags(verbose) + extra + [os.path.join(CSRC, s) for s in SOURCES] + ["-o", out + ".tmp"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    # one object per source file, side by side; those that are up to date are kept
+    os.makedirs(OBJ, exist_ok=True)
+    name = os.path.splitext(os.path.basename(out))[0]
+    compile_flags = [f for f in flags(verbose) if f != "-shared"]
+    objects, running = [], []
+    for src in SOURCES:
+        obj = os.path.join(OBJ, f"{name}.{os.path.splitext(src)[0]}.o")
+        objects.append(obj)
+        if force or _older(obj, PARTS[src]):
+            cmd = [nvcc()] + compile_flags + extra + ["-c", os.path.join(CSRC, src), "-o", obj + ".tmp"]
+            running.append((obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    failed = ""
+    for obj, p in running:
+        said, _ = p.communicate()
+        if p.returncode != 0:
+            failed += said
+        else:
+            os.replace(obj + ".tmp", obj)
+            if verbose:
+                sys.stderr.write(said)
+    if failed:
+        raise RuntimeError("nvcc failed:\n" + failed)
+    r = subprocess.run([nvcc()] + flags() + objects + ["-o", out + ".tmp"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    if verbose:
-        sys.stderr.write(r.stdout + r.stderr)
     os.replace(out + ".tmp", out)
     return out
 

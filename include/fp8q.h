@@ -312,6 +312,153 @@ FP8Q_API fp8q_status fp8_linear_noalloc(const uint8_t* Xq, const float* x_scale,
                                         const float* w_scale, int64_t M, int64_t N, int64_t K, int mode,
                                         void* Y_bf16, int64_t ldy, void* stream);
 
+/* ------------------------------------------- rotary positions, 4-bit KV cache ---
+ *
+ * The attention block between fp8_linear's q/k/v projections and o_proj: queries
+ * are rotated (fp8q_rope), keys and values are appended to a paged cache with
+ * the keys' rotation applied on the way (fp8q_kv4_append), and attention reads
+ * that cache (fp8q_kv4_attention).  Heads are bf16 tensors [T, heads, D] with
+ * contiguous elements and any token and head strides (in elements), so the
+ * parts of a fused q/k/v row are passed as they are.
+ */
+
+enum {
+    FP8Q_ROPE_HALF = 0,           /* pairs (i, i + R/2), R = rot_dim                     */
+    FP8Q_ROPE_INTERLEAVED = 1,    /* pairs (2i, 2i + 1)                                  */
+    FP8Q_ROPE_INVERSE = 2         /* flag: rotate back (also the forward pass's gradient)*/
+};
+
+enum { FP8Q_ROPE_UNSCALED = 0, FP8Q_ROPE_LINEAR = 1, FP8Q_ROPE_LLAMA3 = 2, FP8Q_ROPE_YARN = 3 };
+
+/* How rotary frequencies are stretched for long contexts.  factor >= 1.
+ *   LINEAR   every frequency / factor.
+ *   LLAMA3   with t = original_max_position * f / 2 pi turns over the original
+ *            context: f / factor for t <= low, f for t >= high, linear in t
+ *            between (Llama 3.1: factor 8, low 1, high 4, original 8192).
+ *   YARN     linear in the pair index between the indices that make `high` and
+ *            `low` turns (Peng et al. 2023: beta_fast 32, beta_slow 1); its
+ *            attention factor is the caller's mscale. */
+typedef struct {
+    int type;                     /* FP8Q_ROPE_UNSCALED, _LINEAR, _LLAMA3 or _YARN       */
+    double factor, low, high, original_max_position;
+} fp8q_rope_scaling;
+
+/*
+ * fp8q_rope_frequencies -- the rot_dim / 2 rotary frequencies in radians per
+ * position, theta^(-2i / rot_dim) stretched by `scaling` (NULL: unscaled).
+ * Host only: `freq` is HOST memory; copy it to the device for the calls below.
+ */
+FP8Q_API fp8q_status fp8q_rope_frequencies(double* freq, int64_t rot_dim, double theta,
+                                           const fp8q_rope_scaling* scaling);
+
+/*
+ * fp8q_rope -- rotate bf16 heads X[T, H, D] by their tokens' positions.
+ *   y0 = x0 c - x1 s,  y1 = x1 c + x0 s,  c = mscale cos(a), s = mscale sin(a),
+ *   a = positions[t] * freq[i];  FP8Q_ROPE_INVERSE negates s.
+ * The angle is computed in fp64, the rotation in fp32, rounded once to bf16.
+ *   X_bf16     [T, H, D], read-only; any strides >= 0, 2-byte aligned (16-byte
+ *              aligned rows and rot_dim % 16 == 0 are the fast case).
+ *   positions  [T] int64.      freq  [rot_dim / 2] fp64.
+ *   rot_dim    even, 2 <= rot_dim <= D; elements from rot_dim on are copied.
+ *   flags      FP8Q_ROPE_HALF or _INTERLEAVED, optionally | FP8Q_ROPE_INVERSE.
+ *   mscale     > 0, finite (1 unless the context scaling asks for another).
+ *   Y_bf16     [T, H, D], written; its rows must not overlap each other.  Y may
+ *              be X with the same strides (in place), else must not overlap X.
+ * T == 0 is a no-op.  T * H < 2^31.
+ */
+FP8Q_API fp8q_status fp8q_rope(const void* X_bf16, int64_t T, int64_t H, int64_t D, int64_t x_token_stride,
+                               int64_t x_head_stride, const int64_t* positions, const double* freq, int64_t rot_dim,
+                               int flags, float mscale, void* Y_bf16, int64_t y_token_stride, int64_t y_head_stride,
+                               void* stream);
+
+/*
+ * A paged KV cache of E2M1 codes with an E4M3 scale for each 16 elements.
+ * k_pages and v_pages are device memory [num_pages, kv_heads, page_size * 9 D / 16]
+ * bytes (contiguous, 16-byte aligned); one (page, head) slab is page_size rows
+ * of D/2 code bytes (element 2i in the low nibble of byte i), then page_size
+ * rows of D/16 scale bytes.  A value is E2M1(code) * E4M3(scale) * k_scale (or
+ * v_scale), one static fp32 per tensor: amax / 2688 of a calibration set uses
+ * the formats' whole range (fp8_calibrate_static_scale's result / 6).
+ *   page_size 16, 32, 64, 128 or 256;  D = head_dim 64 or 128.
+ * Slot s is row s % page_size of page s / page_size.
+ */
+typedef struct {
+    void* k_pages;
+    void* v_pages;
+    int64_t num_pages;
+    int32_t page_size, kv_heads, head_dim;
+    float k_scale, v_scale;
+} fp8q_kv4_cache;
+
+/* Bytes of one page of k_pages (or v_pages); 0 for sizes that are not supported. */
+FP8Q_API size_t fp8q_kv4_page_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim);
+
+/*
+ * fp8q_kv4_append -- write T tokens' keys and values into the cache.
+ * K is rotated by its positions in fp64 and rounded once to fp32 (with
+ * positions and freq NULL it is taken as it is).  Then, for each 16 elements x,
+ * each fp32 operation rounded once:
+ *   code_s = E4M3(amax|x| / (6 g)),  s = E4M3(code_s) * g,  g = k_scale or v_scale
+ *   code   = E2M1(x / s), 0 where s = 0   (both round to nearest even and saturate)
+ *   K_bf16, V_bf16  [T, kv_heads, D], read-only, 16-byte aligned, strides % 8 == 0.
+ *   slots           [T] int64.  A negative slot's token is skipped (padding); one
+ *                   past the cache is skipped and sets the device error word.
+ *                   Two tokens of a call must not share a slot.
+ *   positions, freq, rot_dim, flags, mscale  as fp8q_rope, without
+ *                   FP8Q_ROPE_INVERSE; rot_dim % 8 == 0 (else FP8Q_ERR_UNSUPPORTED).
+ * T == 0 is a no-op.  Values must be finite.
+ */
+FP8Q_API fp8q_status fp8q_kv4_append(const fp8q_kv4_cache* cache, const void* K_bf16, int64_t k_token_stride,
+                                     int64_t k_head_stride, const void* V_bf16, int64_t v_token_stride,
+                                     int64_t v_head_stride, const int64_t* slots, int64_t T, const int64_t* positions,
+                                     const double* freq, int64_t rot_dim, int flags, float mscale, void* stream);
+
+/*
+ * fp8q_kv4_read -- the cached keys and values of T slots as bf16 [T, kv_heads, D]
+ * (zeros for a negative slot; one past the cache also sets the device error
+ * word).  16-byte aligned, strides % 8 == 0, rows that do not overlap.
+ */
+FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* slots, int64_t T, void* K_bf16,
+                                   int64_t k_token_stride, int64_t k_head_stride, void* V_bf16,
+                                   int64_t v_token_stride, int64_t v_head_stride, void* stream);
+
+/*
+ * fp8q_kv4_attention -- attention of new tokens over the cache (which already
+ * holds them).  Sequence b has kv_len[b] tokens in the cache, in the pages
+ * page_table[b, 0 .. ), and the query rows q_start[b] .. q_start[b + 1] - 1,
+ * its last tokens: row i of n stands at position kv_len[b] - n + i.
+ *   O[row, h] = sum_j softmax_j(sm_scale * Q[row, h] . k_j) v_j over the keys j < kv_len[b]
+ *               that are visible: j <= position where causal, j > position - window
+ *               where window > 0; head h reads cache head h / (Hq / kv_heads).
+ *   A row that sees no key gets zeros (lse -inf).  Rows that belong to no
+ *   sequence (behind q_start[B]) are left as they were.
+ *   Q_bf16, O_bf16  [T, Hq, D], 16-byte aligned, strides % 8 == 0; O's rows must
+ *                   not overlap.  Q's values must be finite.
+ *   page_table      [B, max_pages] int32, row stride table_stride.
+ *   kv_len          [B] int32, 0 <= kv_len[b] <= max_pages * page_size.
+ *   q_start         [B + 1] int32, ascending, q_start[B] <= T; NULL for one row
+ *                   per sequence (row b is sequence b's; then max_q_len is 1).
+ *   max_q_len       the largest number of rows of a sequence; longer ones set the
+ *                   device error word.  Lengths stay on the device: a captured call
+ *                   can be replayed with other lengths up to these bounds.
+ *   lse             [T, Hq] fp32, written when not NULL: log sum_j exp(sm_scale q.k_j).
+ *   workspace       fp8q_kv4_attention_workspace_size bytes (NULL when that is 0),
+ *                   16-byte aligned, with fp8_linear's contract: zero-filled before
+ *                   its first use, left all zero by every completed call, not
+ *                   shared by concurrent calls.
+ *   A bad length or page index on the device never leads out of the tensors: it
+ *   sets the device error word, and the rows concerned are not to be used.
+ */
+FP8Q_API size_t fp8q_kv4_attention_workspace_size(const fp8q_kv4_cache* cache, int64_t B, int64_t T, int64_t Hq,
+                                                  int64_t max_q_len);
+FP8Q_API fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, int64_t q_token_stride,
+                                        int64_t q_head_stride, int64_t T, int64_t Hq, const int32_t* page_table,
+                                        int64_t table_stride, int64_t max_pages, const int32_t* kv_len,
+                                        const int32_t* q_start, int64_t B, int64_t max_q_len, float sm_scale,
+                                        int causal, int64_t window, void* O_bf16, int64_t o_token_stride,
+                                        int64_t o_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
 /* Library version: major * 10000 + minor * 100 + patch. */
 FP8Q_API int fp8q_version(void);
 
