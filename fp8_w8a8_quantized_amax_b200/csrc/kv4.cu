@@ -57,6 +57,7 @@ fp8q::kv4::Cache device_cache(const fp8q_kv4_cache* c) {
   d.v = static_cast<uint8_t*>(c->v_pages);
   d.pages = c->num_pages;
   d.page_size = c->page_size;
+  d.page_shift = 31 - __builtin_clz(static_cast<unsigned>(c->page_size));
   d.heads = c->kv_heads;
   d.D = c->head_dim;
   d.kg = c->k_scale;
@@ -69,6 +70,35 @@ fp8q_status check_rows(const void* p, int64_t t, int64_t h) {
   if (!p || bad_strides(t, h)) return FP8Q_ERR_INVALID_ARG;
   if (!aligned(p, 16) || t % 8 != 0 || h % 8 != 0) return FP8Q_ERR_MISALIGNED;
   return FP8Q_OK;
+}
+
+// What a call of these sizes launches: 8 nt rows a tile, `ctas` of them, and
+// the workspace: an arrival counter for each item, then two partial results per CTA.
+struct AttentionPlan {
+  int nt, ctas, row_tiles;
+  size_t counters, part;
+  size_t bytes() const { return counters + static_cast<size_t>(2 * ctas) * part; }
+};
+
+AttentionPlan attention_plan(const fp8q_kv4_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_q_len, int sms) {
+  const int64_t rows = (max_q_len < T ? max_q_len : T) * (Hq / c->kv_heads);
+  AttentionPlan a;
+  a.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+  a.ctas = sms * (a.nt == 1 ? 4 : (a.nt == 2 ? 3 : 2));
+  a.row_tiles = static_cast<int>((rows + 8 * a.nt - 1) / (8 * a.nt));
+  a.counters = (static_cast<size_t>(B) * a.row_tiles * c->kv_heads * sizeof(unsigned) + 255) & ~size_t(255);
+  a.part = static_cast<size_t>(8 * a.nt) * (c->head_dim + 2) * sizeof(float);
+  return a;
+}
+
+template <int D, int NT, int CTAS>
+fp8q_status launch_few(const fp8q::kv4::AttnParams& p, int ctas, int dev, void* stream) {
+  constexpr int kWarps = 4;
+  using L = fp8q::kv4::few::Layout<D, NT, kWarps>;
+  auto k = fp8q::kv4::few::attention_kernel<D, NT, kWarps, CTAS>;
+  fp8q_status st = ensure_smem(k, L::kBytes, dev);
+  if (st != FP8Q_OK) return st;
+  return launch(k, dim3(static_cast<unsigned>(ctas)), dim3(L::kThreads), L::kBytes, stream, p);
 }
 
 unsigned blocks_for(int64_t items, int64_t per_block, int64_t most) {
@@ -246,7 +276,10 @@ fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* slots, int
 size_t fp8q_kv4_attention_workspace_size(const fp8q_kv4_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                          int64_t max_q_len) {
   if (check_cache(cache) != FP8Q_OK || B <= 0 || T <= 0 || Hq <= 0 || max_q_len <= 0) return 0;
-  return 0;
+  if (Hq % cache->kv_heads != 0 || T > kInt32Max || Hq > 65536 || T * Hq > kInt32Max || B > 65536) return 0;
+  int dev, sms;
+  if (current_device(&dev, &sms) != FP8Q_OK) return 0;
+  return attention_plan(cache, B, T, Hq, max_q_len, sms).bytes();
 }
 
 fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, int64_t q_token_stride,
@@ -266,7 +299,9 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   if ((st = check_rows(O_bf16, o_token_stride, o_head_stride)) != FP8Q_OK) return st;
   if (rows_overlap(T, Hq, cache->head_dim, o_token_stride, o_head_stride)) return FP8Q_ERR_INVALID_ARG;
   if (!page_table || !kv_len || (B > 1 && table_stride < max_pages)) return FP8Q_ERR_INVALID_ARG;
-  if (!aligned(page_table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(lse, 4))
+  if (!workspace) return FP8Q_ERR_INVALID_ARG;   // its size needs the device; presence and alignment do not
+  if (!aligned(page_table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(lse, 4) ||
+      !aligned(workspace, 16))
     return FP8Q_ERR_MISALIGNED;
   if (T > kInt32Max || Hq > 65536 || T * Hq > kInt32Max || B > 65536 || table_stride > kStrideMax ||
       max_pages > kInt32Max || max_pages * cache->page_size > kInt32Max)
@@ -292,13 +327,22 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   p.group = static_cast<int>(Hq / cache->kv_heads);
   p.max_pages = static_cast<int>(max_pages);
   p.max_q = static_cast<int>(max_q_len < T ? max_q_len : T);
-  p.scale = sm_scale * cache->k_scale;
+  p.scale = sm_scale * cache->k_scale * 1.44269504088896340736f;
   p.causal = causal;
   p.window = window;
-  (void)workspace;
-  (void)workspace_bytes;
-  auto k = cache->head_dim == 64 ? fp8q::kv4::attention_kernel<64> : fp8q::kv4::attention_kernel<128>;
-  return launch(k, dim3(static_cast<unsigned>(T * Hq)), dim3(128), 0, stream, p);
+  const AttentionPlan plan = attention_plan(cache, B, T, Hq, max_q_len, sms);
+  if (workspace_bytes < plan.bytes()) return FP8Q_ERR_INVALID_ARG;
+  p.count = static_cast<unsigned*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.counters);
+  p.row_tiles = plan.row_tiles;
+  if (cache->head_dim == 128) {
+    if (plan.nt == 1) return launch_few<128, 1, 4>(p, plan.ctas, dev, stream);
+    if (plan.nt == 2) return launch_few<128, 2, 3>(p, plan.ctas, dev, stream);
+    return launch_few<128, 4, 2>(p, plan.ctas, dev, stream);
+  }
+  if (plan.nt == 1) return launch_few<64, 1, 4>(p, plan.ctas, dev, stream);
+  if (plan.nt == 2) return launch_few<64, 2, 3>(p, plan.ctas, dev, stream);
+  return launch_few<64, 4, 2>(p, plan.ctas, dev, stream);
 }
 
 }  // extern "C"

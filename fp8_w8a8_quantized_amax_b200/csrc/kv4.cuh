@@ -27,7 +27,7 @@ struct Cache {
   uint8_t* k;
   uint8_t* v;
   int64_t pages;
-  int page_size, heads, D;
+  int page_size, page_shift, heads, D;
   float kg, vg;
   __host__ __device__ int64_t slab() const { return static_cast<int64_t>(page_size) * (D * 9 / 16); }
   __host__ __device__ int64_t code_offset(int64_t page, int head, int row) const {

@@ -3,7 +3,8 @@
 // For query row i of sequence b (n_b rows, the last n_b of its kv_len tokens):
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(sm_scale q.k_j - m),
 // over the visible keys j: j < kv_len; causal: j <= pos, pos = kv_len - n_b + i;
-// a window W: j > pos - W.  One pass: running maximum m and sum, rescaled when m grows.
+// a window W: j > pos - W.  One pass over the cache: running maximum m and sum
+// in fp32, the sums rescaled when m grows.
 #pragma once
 
 #include "kv4.cuh"
@@ -19,12 +20,16 @@ struct AttnParams {
   const int32_t* table;
   const int32_t* kv_len;
   const int32_t* q_start;   // nullptr: one row per sequence
+  unsigned* count;          // workspace: arrivals per (sequence, row tile, head)
+  float* part;              // workspace: two partial results per CTA
   int64_t qt, qh, ot, oh, table_stride;
-  int T, B, Hq, group, max_pages, max_q;
-  float scale;              // sm_scale * g_k
+  int T, B, Hq, group, max_pages, max_q, row_tiles;
+  float scale;              // sm_scale * g_k * log2(e)
   int causal;
   int64_t window;           // 0: none
 };
+
+constexpr float kLn2 = 0.693147180559945309f;
 
 // The rows [r0, r0 + n) and cached tokens of sequence b, bounded to what the
 // tensors hold (a length that has to be cut sets the error word).
@@ -46,91 +51,654 @@ __device__ __forceinline__ Seq sequence(const AttnParams& p, int b) {
 }
 
 // Visible keys [first, last) of the row at position pos.
-__device__ __forceinline__ void visible(const AttnParams& p, const Seq& s, int pos, int* first, int* last) {
-  *last = p.causal ? min(s.kv, pos + 1) : s.kv;
-  const int64_t f = p.window > 0 ? static_cast<int64_t>(pos) - p.window + 1 : 0;
-  *first = f > 0 ? static_cast<int>(min(f, static_cast<int64_t>(0x7FFFFFFF))) : 0;
+__device__ __forceinline__ int visible_first(const AttnParams& p, int pos) {
+  if (p.window <= 0) return 0;
+  const int64_t f = static_cast<int64_t>(pos) - p.window + 1;
+  return f > 0 ? static_cast<int>(f) : 0;
+}
+__device__ __forceinline__ int visible_last(const AttnParams& p, const Seq& s, int pos) {
+  return p.causal ? max(0, min(s.kv, pos + 1)) : s.kv;
 }
 
-// One CTA per (row, query head), its four warps taking every fourth key; a
-// lane holds D/32 dimensions.
-template <int D>
-__global__ void __launch_bounds__(128) attention_kernel(AttnParams p) {
-  constexpr int E = D / 32;
-  __shared__ float red_m[4], red_l[4], red_o[4][D];
+// ------------------------------------------------------------ few rows ---
+//
+// Up to 8 NT query rows per key head (the group's heads times the new tokens)
+// meet every cached key, so the work is the stream of the cache: 9 D / 8 bytes
+// per key and head.  Matrix instructions keep the products off the CUDA cores;
+// with at most 8 NT columns they are mma.sync m16n8k16 with the keys (then the
+// dimensions) as rows: the dequantized operand goes straight from registers
+// into the instruction, where tcgen05 would want it written back to shared
+// memory first.
+//   S^T [16 keys, 8 rows]  = K [16 keys, D] . Q^T       (A = K, dequantized)
+//   O^T [16 dims, 8 rows] += V^T [16 dims, 16 keys] . P^T  (A = V^T)
+// Both contractions may go over their index in any order as long as both
+// operands agree, so each lane takes a contiguous run of a cache row: of K's
+// rows 32 elements (one 16-byte load, two scales), of V's rows 16 (one scale).
+// V^T's operand pairs two keys in a register: the two keys' nibbles are merged
+// into bytes (two logic operations for four values) before they are widened.
+// E2M1 times E4M3 is exact in f16.  Q is scaled by a power of two per row so
+// that its bf16 values are f16 values (all of them that are not below 2^-38 of
+// the row's largest); P, at most 1, is rounded to f16.
+//
+// The keys of a (sequence, key head) are cut into steps of WARPS * 32; the
+// list of all steps is cut evenly over the CTAs (stream-K, as in the linear's
+// decode kernel), whatever the lengths.  A warp takes 32 keys of each step
+// through its own two-stage ring of bulk copies and keeps its own running
+// maximum, sum and O^T; the warps' results are joined where an item ends.  An
+// item cut between CTAs is joined by the last of them to finish, in CTA order.
+namespace few {
+
+constexpr int kTile = 32;     // keys of a warp per step
+constexpr int kStages = 2;
+
+template <int D, int NT, int WARPS>
+struct Layout {
+  static constexpr int kThreads = 32 * WARPS;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStep = WARPS * kTile;
+  static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
+  static constexpr int kStageBytes = 2 * (kCodes + kScales);       // K codes, K scales, V codes, V scales
+  static constexpr int kRedStride = D + 4;
+  static constexpr int kRed = WARPS * kStages * kStageBytes;       // [WARPS][kRows][kRedStride] fp32
+  static constexpr int kMl = kRed + WARPS * kRows * kRedStride * 4;   // [WARPS][kRows] m, then l
+  static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // NT = 4: Q fragments
+  static constexpr int kBars = kQ + (NT == 4 ? NT * (D / 16) * 32 * 8 : 0);
+  static constexpr int kMisc = kBars + WARPS * kStages * 8;
+  static constexpr int kBytes = kMisc + 128;
+  static constexpr int kPart = kRows * (D + 2);                    // floats of a partial result
+};
+
+struct Range {
+  int64_t q, r;   // CTA c takes q + 1 steps when c < r, else q
+  __device__ int64_t begin(int64_t c) const { return c * q + min(c, r); }
+  __device__ int owner(int64_t s) const {
+    const int64_t big = r * (q + 1);
+    return static_cast<int>(s < big ? s / (q + 1) : r + (s - big) / q);
+  }
+};
+
+// A sequence's keys [first, hi) that some row sees, lo (first rounded down to a
+// tile), the steps they make and the number of items (row tiles times key heads).
+struct Span {
+  Seq s;
+  int first, lo, hi, steps, items;
+};
+
+template <int ROWS, int STEP>
+__device__ __forceinline__ Span span(const AttnParams& p, int b) {
+  Span x;
+  x.s = sequence(p, b);
+  x.hi = x.s.kv;
+  x.first = visible_first(p, x.s.kv - x.s.n);
+  x.lo = x.first & ~(kTile - 1);
+  x.steps = max(1, (x.hi - x.lo + STEP - 1) / STEP);
+  x.items = x.s.n > 0 ? (x.s.n * p.group + ROWS - 1) / ROWS * p.c.heads : 0;
+  return x;
+}
+
+// A place in the list of steps.
+template <int ROWS, int STEP>
+struct Place {
+  Span x;
+  int b, item, step;
+  __device__ void enter(const AttnParams& p) {     // the first sequence from b on that has rows
+    x.items = 0;
+    while (b < p.B) {
+      x = span<ROWS, STEP>(p, b);
+      if (x.items > 0) break;
+      ++b;
+    }
+  }
+  __device__ void next(const AttnParams& p) {
+    if (++step < x.steps) return;
+    step = 0;
+    if (++item < x.items) return;
+    item = 0;
+    ++b;
+    enter(p);
+  }
+};
+
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A power of two that brings a value of magnitude amax to [2^14, 2^15) (as far
+// as fp32 has it), by its exponent k.
+__device__ __forceinline__ int row_exponent(float amax) {
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23);
+  return amax > 0.0f ? min(126, 141 - e) : 0;
+}
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
+
+template <int D, int NT, int WARPS, int CTAS>
+__global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(AttnParams p) {
+  using L = Layout<D, NT, WARPS>;
+  constexpr int kRows = L::kRows, kStep = L::kStep, kSteps = D / 16;
+  using Where = Place<kRows, kStep>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = lane_id(), warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  float* red = reinterpret_cast<float*>(smem + L::kRed);
+  float* ml = reinterpret_cast<float*>(smem + L::kMl);
+  uint2* qs = reinterpret_cast<uint2*>(smem + L::kQ);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars) + warp * kStages;
+  int64_t* misc = reinterpret_cast<int64_t*>(smem + L::kMisc);
+  volatile int* abort = reinterpret_cast<int*>(smem + L::kMisc + 96);
+  if (threadIdx.x == 0) *abort = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = lane_id(), warp = threadIdx.x >> 5;
-  const int h = blockIdx.x % p.Hq, kvh = h / p.group;
-  const int row = blockIdx.x / p.Hq;
-  // the sequence that holds this row
-  int b = -1;
-  Seq s = {0, 0, 0};
-  for (int i = 0; i < p.B; ++i) {
-    const Seq c = sequence(p, i);
-    if (row >= c.r0 && row < c.r0 + c.n) {
-      b = i;
-      s = c;
+
+  // ---- this CTA's range of the list: a scan over the sequences' steps ----
+  int64_t total = 0, before = 0;     // before: steps ahead of this thread's sequence, in the last chunk scanned
+  int64_t mine = 0;
+  auto scan = [&](int base) {
+    const int b = base + static_cast<int>(threadIdx.x);
+    mine = 0;
+    if (b < p.B) {
+      const Span x = span<kRows, kStep>(p, b);
+      mine = static_cast<int64_t>(x.items) * x.steps;
+    }
+    int64_t v = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) misc[warp] = v;
+    __syncthreads();
+    int64_t ahead = 0, all = 0;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) ahead += misc[w];
+      all += misc[w];
+    }
+    before = ahead + v - mine;
+    return all;
+  };
+  for (int base = 0; base < p.B; base += L::kThreads) total += scan(base);
+  Range range;
+  range.q = total / gridDim.x;
+  range.r = total - range.q * gridDim.x;
+  const int64_t begin = range.begin(blockIdx.x);
+  const int64_t end = range.begin(blockIdx.x + 1);
+  if (begin == end) return;
+  {
+    int64_t ahead = 0;
+    for (int base = 0; base < p.B; base += L::kThreads) {
+      const int64_t all = p.B <= L::kThreads ? total : scan(base);
+      if (begin >= ahead && begin < ahead + all) {
+        const int64_t at = begin - ahead - before;
+        __syncthreads();
+        if (at >= 0 && at < mine) {
+          misc[8] = base + threadIdx.x;
+          misc[9] = at;
+        }
+        __syncthreads();
+        break;
+      }
+      ahead += all;
     }
   }
-  if (b < 0) return;                       // a row behind the last sequence
-  int first, last;
-  visible(p, s, s.kv - s.n + row - s.r0, &first, &last);
-  float q[E], acc[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = bf16lo(p.q[row * p.qt + h * p.qh + lane * E + i]) * p.scale;
-    acc[i] = 0.0f;
+  Where cur;
+  cur.b = static_cast<int>(misc[8]);
+  cur.x = span<kRows, kStep>(p, cur.b);
+  {
+    const int64_t at = misc[9];
+    cur.item = static_cast<int>(at / cur.x.steps);
+    cur.step = static_cast<int>(at - static_cast<int64_t>(cur.item) * cur.x.steps);
   }
-  float m = -INFINITY, l = 0.0f;
-  for (int j = first + warp; j < last; j += 4) {
-    const int page = p.table[b * p.table_stride + j / p.c.page_size];
-    if (page < 0 || page >= p.c.pages) {
-      atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadPage));
-      continue;
+
+  // ---- loads: the warp's tile of a step, from up to two pages ----
+  const int chunk = min(p.c.page_size, kTile), chunks = kTile / chunk;
+  const uint64_t policy = policy_evict_first();
+  int pending = 0;                                  // stages with copies in flight
+  uint8_t* stages = smem + warp * kStages * L::kStageBytes;
+  const int64_t slab = p.c.slab();
+  auto tile_of = [&](const Where& w) { return w.x.lo + w.step * kStep + warp * kTile; };
+  // this lane's page of a tile (lanes 0 .. 4 * chunks - 1: a chunk's four parts)
+  auto page_of = [&](const Where& w) {
+    const int key = tile_of(w) + (lane >> 2) * chunk;
+    int page = 0;
+    if (lane < 4 * chunks && key < w.x.hi && key + chunk > w.x.first)
+      page = p.table[w.b * p.table_stride + (key >> p.c.page_shift)];
+    return page;
+  };
+  auto issue = [&](const Where& w, int page, int stage) {
+    const int k0 = tile_of(w);
+    if (k0 >= w.x.hi || *abort) return;
+    // of a first tile, 16-key pages ahead of the first key are left out; of a last one, those behind the last key
+    const int c0 = chunks == 2 && w.x.first >= k0 + chunk ? 1 : 0;
+    const int c1 = chunks == 2 && w.x.hi <= k0 + chunk ? 1 : chunks;
+    if (lane == 0) mbar_arrive_expect_tx(&bars[stage], (c1 - c0) * chunk * (D * 9 / 8));
+    __syncwarp();
+    pending |= 1 << stage;
+    const int c = lane >> 2, part = lane & 3;
+    if (c >= c0 && c < c1) {
+      if (page < 0 || page >= p.c.pages) {
+        atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadPage));
+        page = 0;
+      }
+      const int row = (k0 + c * chunk) & (p.c.page_size - 1);
+      const int head = w.item % p.c.heads;
+      const uint8_t* src = ((part & 2) ? p.c.v : p.c.k) + (static_cast<int64_t>(page) * p.c.heads + head) * slab;
+      uint8_t* dst = stages + stage * L::kStageBytes + ((part & 2) ? L::kCodes + L::kScales : 0);
+      if (part & 1)
+        bulk_load(dst + L::kCodes + c * chunk * (D / 16), src + p.c.page_size * (D / 2) + row * (D / 16),
+                  chunk * (D / 16), &bars[stage], policy);
+      else
+        bulk_load(dst + c * chunk * (D / 2), src + row * (D / 2), chunk * (D / 2), &bars[stage],
+                  policy);
     }
-    const int r = j % p.c.page_size;
-    float k[E], v[E];
-    const int64_t at = p.c.code_offset(page, kvh, r) + lane * E / 2, sat = p.c.scale_offset(page, kvh, r) + lane * E / 16;
-    const float ks = f16lo(widen_e4m3x2(p.c.k[sat])), vs = f16lo(widen_e4m3x2(p.c.v[sat]));
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const uint32_t kw = widen_e2m1x2(p.c.k[at + i / 2]), vw = widen_e2m1x2(p.c.v[at + i / 2]);
-      k[i] = f16lo(kw) * ks;
-      k[i + 1] = f16hi(kw) * ks;
-      v[i] = f16lo(vw) * vs;
-      v[i + 1] = f16hi(vw) * vs;
+  };
+
+  // ---- the walk ----
+  Where ahead = cur;
+  int64_t s_ahead = begin;
+  int next_page = page_of(ahead);
+  int phase = 0, stage_in = 0, stage_out = 0;      // bit i of phase: stage i's parity
+  auto advance = [&]() {                            // issue the next step's tile, look its successor's page up
+    if (s_ahead >= end) return;
+    issue(ahead, next_page, stage_in);
+    stage_in ^= 1;
+    if (++s_ahead < end) {
+      ahead.next(p);
+      next_page = page_of(ahead);
     }
-    float x = 0.0f;
+  };
+  advance();
+
+  uint32_t qf[NT == 4 ? 1 : NT][kSteps][2];
+  float qscale[NT][2];
+  int first[NT][2], last[NT][2];
+  float m[NT][2], l[NT][2];
+  float o[kSteps][NT][4];
+  int all_first = 0, all_last = 0;                  // keys that every row of the item sees
+  bool fresh = true;
+  const int64_t seg_first = begin;
+  int64_t seg = begin;                              // first step of the current segment
+
+  for (int64_t s = begin; s < end; ++s) {
+    advance();
+    if (fresh) {
+      // the item's query rows: lane (g, t) holds row 8 nt + g, elements [t D/4, (t + 1) D/4)
+      fresh = false;
+      seg = s;
+      const int head = cur.item % p.c.heads, row0 = cur.item / p.c.heads * kRows;
+      const int rows = cur.x.s.n * p.group;
+      if constexpr (NT == 4) __syncthreads();       // the previous item's fragments are no longer read
 #pragma unroll
-    for (int i = 0; i < E; ++i) x = fmaf(q[i], k[i], x);
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = row0 + nt * 8 + g;
+        uint32_t w[D / 8];
+        if (r < rows) {
+          const uint16_t* src = p.q + (cur.x.s.r0 + r / p.group) * p.qt + (head * p.group + r % p.group) * p.qh + t * (D / 4);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    const float mn = fmaxf(m, x), w = expf(x - mn), f = expf(m - mn);
-    m = mn;
-    l = l * f + w;
+          for (int i = 0; i < D / 32; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+          }
+        } else {
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = fmaf(w, v[i], acc[i] * f);
+          for (int i = 0; i < D / 8; ++i) w[i] = 0;
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const int k = row_exponent(amax);
+        const float up = pow2(k), down = pow2(-k) * p.scale;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const uint32_t b0 = pack_f16x2(bf16lo(w[2 * i]) * up, bf16hi(w[2 * i]) * up);
+          const uint32_t b1 = pack_f16x2(bf16lo(w[2 * i + 1]) * up, bf16hi(w[2 * i + 1]) * up);
+          if constexpr (NT == 4) {
+            if (warp == 0) qs[(nt * kSteps + i) * 32 + lane] = make_uint2(b0, b1);
+          } else {
+            qf[nt][i][0] = b0;
+            qf[nt][i][1] = b1;
+          }
+        }
+        qscale[nt][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
+        qscale[nt][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = row0 + nt * 8 + 2 * t + i;
+          const int pos = cur.x.s.kv - cur.x.s.n + row / p.group;
+          first[nt][i] = visible_first(p, pos);
+          last[nt][i] = row < rows ? visible_last(p, cur.x.s, pos) : 0;
+          m[nt][i] = -INFINITY;
+          l[nt][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+      }
+      all_last = visible_last(p, cur.x.s, cur.x.s.kv - cur.x.s.n + row0 / p.group);
+      all_first = visible_first(p, cur.x.s.kv - cur.x.s.n + (min(rows, row0 + kRows) - 1) / p.group);
+      if constexpr (NT == 4) __syncthreads();
+    }
+
+    const int k0 = tile_of(cur);
+    if (k0 < cur.x.hi) {
+      if (!*abort && mbar_wait(&bars[stage_out], (phase >> stage_out) & 1, abort, kErrWaitFull)) {
+        phase ^= 1 << stage_out;
+        pending &= ~(1 << stage_out);
+      }
+      const uint8_t* kc = stages + stage_out * L::kStageBytes;
+      const uint8_t* ks = kc + L::kCodes;
+      const uint8_t* vc = ks + L::kScales;
+      const uint8_t* vs = vc + L::kCodes;
+      const bool whole = k0 >= all_first && k0 + kTile <= all_last;
+      // Row r of a 16-key tile is key r ^ (r / 4 & 1): K's rows of neighbouring lane groups and V's rows 2t (and
+      // 2t + 1) of the four t then lie in different banks (V: at most two lanes to a bank).
+      const int kg = g ^ ((g >> 2) & 1);
+      float sc[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[mt][nt][i] = 0.0f;
+        const int r0 = mt * 16 + kg, r1 = r0 + 8;
+        uint32_t w0[D / 32], w1[D / 32], s0[2], s1[2];
+        if constexpr (D == 128) {
+          const uint4 a = *reinterpret_cast<const uint4*>(kc + r0 * 64 + t * 16);
+          const uint4 b = *reinterpret_cast<const uint4*>(kc + r1 * 64 + t * 16);
+          w0[0] = a.x; w0[1] = a.y; w0[2] = a.z; w0[3] = a.w;
+          w1[0] = b.x; w1[1] = b.y; w1[2] = b.z; w1[3] = b.w;
+          const uint32_t x = widen_e4m3x2(*reinterpret_cast<const uint16_t*>(ks + r0 * 8 + t * 2));
+          const uint32_t y = widen_e4m3x2(*reinterpret_cast<const uint16_t*>(ks + r1 * 8 + t * 2));
+          s0[0] = __byte_perm(x, x, 0x1010); s0[1] = __byte_perm(x, x, 0x3232);
+          s1[0] = __byte_perm(y, y, 0x1010); s1[1] = __byte_perm(y, y, 0x3232);
+        } else {
+          const uint2 a = *reinterpret_cast<const uint2*>(kc + r0 * 32 + t * 8);
+          const uint2 b = *reinterpret_cast<const uint2*>(kc + r1 * 32 + t * 8);
+          w0[0] = a.x; w0[1] = a.y;
+          w1[0] = b.x; w1[1] = b.y;
+          const uint32_t x = widen_e4m3x2(ks[r0 * 4 + t] | (static_cast<uint32_t>(ks[r1 * 4 + t]) << 8));
+          s0[0] = s0[1] = __byte_perm(x, x, 0x1010);
+          s1[0] = s1[1] = __byte_perm(x, x, 0x3232);
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          uint32_t a[4], b[4];
+          widen4(w0[w], a);
+          widen4(w1[w], b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a[j] = mul_f16x2(a[j], s0[w / 2]);
+            b[j] = mul_f16x2(b[j], s1[w / 2]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t b0, b1;
+              if constexpr (NT == 4) {
+                const uint2 v = qs[(nt * kSteps + 2 * w + h) * 32 + lane];
+                b0 = v.x;
+                b1 = v.y;
+              } else {
+                b0 = qf[nt][2 * w + h][0];
+                b1 = qf[nt][2 * w + h][1];
+              }
+              mma16816(sc[mt][nt], a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1], b0, b1);
+            }
+        }
+      }
+      // softmax over the tile: element i of sc is key (g, g + 8)[i / 2], row 2t + i % 2
+      uint32_t pf[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = sc[mt][nt][i] * qscale[nt][i & 1];
+            if (!whole) {
+              const int key = k0 + mt * 16 + kg + (i >> 1) * 8;
+              v = key >= first[nt][i & 1] && key < last[nt][i & 1] ? v : -INFINITY;
+            }
+            sc[mt][nt][i] = v;
+            top[i & 1] = fmaxf(top[i & 1], v);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], d));
+          top[i] = fmaxf(top[i], m[nt][i]);
+        }
+        if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] || top[1] > m[nt][1])) {
+          float f[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            f[i] = top[i] > m[nt][i] ? ex2(m[nt][i] - top[i]) : 1.0f;      // 0 from -infinity
+            l[nt][i] *= f[i];
+            m[nt][i] = top[i];
+          }
+#pragma unroll
+          for (int d = 0; d < kSteps; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][nt][i] *= f[i & 1];
+        }
+        const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[mt][nt][i] = ex2(sc[mt][nt][i] - base[i & 1]);
+            l[nt][i & 1] += sc[mt][nt][i];
+          }
+          pf[mt][nt][0] = transpose8x8(pack_f16x2(sc[mt][nt][0], sc[mt][nt][1]));
+          pf[mt][nt][1] = transpose8x8(pack_f16x2(sc[mt][nt][2], sc[mt][nt][3]));
+        }
+      }
+      // V^T: row g (and g + 8) of m-tile i is element g D/8 + 2i (and + 1); columns 2t, 2t + 1 (and + 8) are keys
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        int key[4];
+        key[0] = mt * 16 + (2 * t ^ (t >> 1));
+        key[1] = mt * 16 + ((2 * t + 1) ^ (t >> 1));
+        key[2] = key[0] + 8;
+        key[3] = key[1] + 8;
+        uint32_t vw[4][D / 64], sv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (D == 128) {
+            const uint2 a = *reinterpret_cast<const uint2*>(vc + key[i] * 64 + g * 8);
+            vw[i][0] = a.x;
+            vw[i][1] = a.y;
+            sv[i] = vs[key[i] * 8 + g];
+          } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(vc + key[i] * 32 + g * 4);
+            sv[i] = vs[key[i] * 4 + (g >> 1)];
+          }
+          // what lies outside the keys, or was not loaded, need not be a number that times zero is zero
+          if (!whole && (k0 + key[i] >= cur.x.hi || k0 + key[i] < cur.x.first)) sv[i] = 0;
+        }
+        const uint32_t s01 = widen_e4m3x2(sv[0] | (sv[1] << 8)), s23 = widen_e4m3x2(sv[2] | (sv[3] << 8));
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          uint32_t e0[4], e1[4], e2[4], e3[4];
+          widen4((vw[0][w] & 0x0F0F0F0Fu) | ((vw[1][w] << 4) & 0xF0F0F0F0u), e0);
+          widen4(((vw[0][w] >> 4) & 0x0F0F0F0Fu) | (vw[1][w] & 0xF0F0F0F0u), e1);
+          widen4((vw[2][w] & 0x0F0F0F0Fu) | ((vw[3][w] << 4) & 0xF0F0F0F0u), e2);
+          widen4(((vw[2][w] >> 4) & 0x0F0F0F0Fu) | (vw[3][w] & 0xF0F0F0F0u), e3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e0[j] = mul_f16x2(e0[j], s01);
+            e1[j] = mul_f16x2(e1[j], s01);
+            e2[j] = mul_f16x2(e2[j], s23);
+            e3[j] = mul_f16x2(e3[j], s23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(o[4 * w + j][nt], e0[j], e1[j], e2[j], e3[j], pf[mt][nt][0], pf[mt][nt][1]);
+          }
+        }
+      }
+      __syncwarp();                                 // every lane has read the stage before it is filled again
+    }
+    stage_out ^= 1;
+
+    // ---- the end of the item, or of the CTA's range ----
+    const bool item_ends = cur.step + 1 == cur.x.steps;
+    if (item_ends || s + 1 == end) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) l[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][i], d);
+          if (g == 0) {
+            const int r = nt * 8 + 2 * t + i;
+            ml[warp * kRows + r] = m[nt][i];
+            ml[(WARPS + warp) * kRows + r] = l[nt][i];
+          }
+        }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * t + i;
+          float top = -INFINITY;
+          for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
+          const float f = m[nt][i] == -INFINITY ? 0.0f : ex2(m[nt][i] - top);
+          float* dst = red + (warp * kRows + r) * L::kRedStride + g * (D / 8);
+#pragma unroll
+          for (int d = 0; d < kSteps; d += 2)
+            *reinterpret_cast<float4*>(dst + 2 * d) = make_float4(o[d][nt][i] * f, o[d][nt][i + 2] * f,
+                                                                  o[d + 1][nt][i] * f, o[d + 1][nt][i + 2] * f);
+        }
+      }
+      __syncthreads();
+      const int head = cur.item % p.c.heads, row0 = cur.item / p.c.heads * kRows;
+      const int rows = min(kRows, cur.x.s.n * p.group - row0);
+      const int64_t i0 = s - cur.step, i1 = i0 + cur.x.steps;     // the item's steps in the list
+      const bool split = i0 < begin || i1 > end;
+      auto finish = [&](int r, int d, float4 v, float top, float sum) {
+        const int row = row0 + r;
+        const int64_t token = cur.x.s.r0 + row / p.group;
+        const int h = head * p.group + row % p.group;
+        const float f = sum > 0.0f ? p.c.vg / sum : 0.0f;
+        uint2 w;
+        w.x = pack_bf16x2(v.x * f, v.y * f);
+        w.y = pack_bf16x2(v.z * f, v.w * f);
+        *reinterpret_cast<uint2*>(p.o + token * p.ot + h * p.oh + d) = w;
+        if (p.lse && d == 0) p.lse[token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+      };
+      float* slot = split ? p.part + (2 * static_cast<int64_t>(blockIdx.x) + (seg == seg_first ? 0 : 1)) * L::kPart
+                          : nullptr;
+      for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float top = -INFINITY, sum = 0.0f;
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 0; w < WARPS; ++w) {
+          const float mw = ml[w * kRows + r];
+          if (mw != -INFINITY) sum += ml[(WARPS + w) * kRows + r] * ex2(mw - top);
+          const float4 x = *reinterpret_cast<const float4*>(red + (w * kRows + r) * L::kRedStride + d);
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+        if (!split) {
+          finish(r, d, v, top, sum);
+        } else {
+          __stcg(reinterpret_cast<float4*>(slot + r * D + d), v);
+          if (d == 0) {
+            __stcg(slot + kRows * D + r, top);
+            __stcg(slot + kRows * (D + 1) + r, sum);
+          }
+        }
+      }
+      if (split) {
+        const int c0 = range.owner(i0), c1 = range.owner(i1 - 1);
+        unsigned* count = p.count + (static_cast<int64_t>(cur.b) * p.row_tiles) * p.c.heads + cur.item;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) misc[10] = atom_add_acq_rel_gpu(count, 1u);
+        __syncthreads();
+        if (static_cast<int>(misc[10]) == c1 - c0) {              // every other part is in
+          __threadfence();
+          for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            float top = -INFINITY, sum = 0.0f;
+            auto part = [&](int c) { return p.part + (2 * static_cast<int64_t>(c) + (c == c0 && range.begin(c0) != i0 ? 1 : 0)) * L::kPart; };
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part(c) + kRows * D + r));
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int c = c0; c <= c1; ++c) {
+              float* src = part(c);
+              const float mw = __ldcg(src + kRows * D + r);
+              const float f = mw == -INFINITY ? 0.0f : ex2(mw - top);
+              sum += __ldcg(src + kRows * (D + 1) + r) * f;
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
+              v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+            }
+            finish(r, d, v, top, sum);
+          }
+          __syncthreads();
+          for (int c = c0; c <= c1; ++c) {                        // the workspace is left all zero
+            float* dst = p.part + (2 * static_cast<int64_t>(c) + (c == c0 && range.begin(c0) != i0 ? 1 : 0)) * L::kPart;
+            for (int i = threadIdx.x; i < L::kPart; i += L::kThreads) __stcg(dst + i, 0.0f);
+          }
+          if (threadIdx.x == 0) *count = 0;
+        }
+      }
+      fresh = true;
+      __syncthreads();                              // red, ml and misc are free again
+    }
+    cur.next(p);
   }
-  if (lane == 0) {
-    red_m[warp] = m;
-    red_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i) red_o[warp][lane * E + i] = acc[i];
-  __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, red_m[w]);
-  for (int w = 0; w < 4; ++w)
-    if (red_l[w] > 0.0f) sum += red_l[w] * expf(red_m[w] - top);
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float o = 0.0f;
-    for (int w = 0; w < 4; ++w)
-      if (red_l[w] > 0.0f) o += red_o[w][d] * expf(red_m[w] - top);
-    p.o[row * p.ot + h * p.oh + d] = static_cast<uint16_t>(pack_bf16x2(sum > 0.0f ? o / sum * p.c.vg : 0.0f, 0.0f));
-  }
-  if (p.lse && threadIdx.x == 0) p.lse[static_cast<int64_t>(row) * p.Hq + h] = top + logf(sum);
+  // A wait that ran out: the copies still in flight land before the shared memory is given back.
+  if (*abort)
+    for (int i = 0; i < kStages; ++i)
+      if ((pending >> i) & 1) mbar_wait_drain(&bars[i], (phase >> i) & 1, kErrWaitDrain);
 }
+
+}  // namespace few
 
 }  // namespace kv4
 }  // namespace fp8q

@@ -216,6 +216,7 @@ def test_read_arguments(L, kw, want):
     (dict(q=P + 8), MIS), (dict(o=P + 8), MIS), (dict(table=P + 2), MIS), (dict(kv=P + 2), MIS), (dict(qs=P + 2), MIS),
     (dict(lse=P + 2), MIS), (dict(lse=P), VALID), (dict(qt=4100), MIS), (dict(oh=132, ot=8192), MIS),
     (dict(ot=0), INV), (dict(oh=64), INV), (dict(ts=15), INV), (dict(B=1, ts=0), VALID),
+    (dict(ws=None), INV), (dict(ws=P + 8), MIS),
     (dict(qs=None), INV),                                      # one row per sequence: max_q_len is 1
     (dict(qs=None, mq=1), VALID), (dict(qs=None, mq=1, T=2), INV),
     (dict(B=70000, T=70000), UNS), (dict(mp=1 << 30, ts=1 << 30), UNS), (dict(T=1 << 27, Hq=32, ot=4096), UNS),
