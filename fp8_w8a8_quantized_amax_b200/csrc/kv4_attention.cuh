@@ -90,6 +90,7 @@ namespace few {
 
 constexpr int kTile = 32;     // keys of a warp per step
 constexpr int kStages = 2;
+constexpr float kSlack = 8.0f;
 
 template <int D, int NT, int WARPS>
 struct Layout {
@@ -104,7 +105,8 @@ struct Layout {
   static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // NT = 4: Q fragments
   static constexpr int kBars = kQ + (NT == 4 ? NT * (D / 16) * 32 * 8 : 0);
   static constexpr int kMisc = kBars + WARPS * kStages * 8;
-  static constexpr int kBytes = kMisc + 128;
+  static constexpr int kJobs = kMisc + 128;                        // two jobs of at most 64 bytes
+  static constexpr int kBytes = kJobs + 128;
   static constexpr int kPart = kRows * (D + 2);                    // floats of a partial result
 };
 
@@ -136,28 +138,32 @@ __device__ __forceinline__ Span span(const AttnParams& p, int b) {
   return x;
 }
 
-// A place in the list of steps.
-template <int ROWS, int STEP>
-struct Place {
+// A CTA's part of one item: `steps` steps from key `key` on, its number in the
+// list, and what the item is.
+struct Job {
   Span x;
-  int b, item, step;
-  __device__ void enter(const AttnParams& p) {     // the first sequence from b on that has rows
-    x.items = 0;
-    while (b < p.B) {
-      x = span<ROWS, STEP>(p, b);
-      if (x.items > 0) break;
-      ++b;
-    }
-  }
-  __device__ void next(const AttnParams& p) {
-    if (++step < x.steps) return;
-    step = 0;
-    if (++item < x.items) return;
-    item = 0;
-    ++b;
-    enter(p);
-  }
+  int b, item, step, steps, key;
+  int64_t s;                 // the part's first step in the list
 };
+static_assert(sizeof(Job) <= 64, "two of them in the layout");
+
+// The job that starts at step s of the list, in sequence b, item `item` (both
+// may be one past their end) and step `step`; the CTA's range ends at `end`.
+template <int ROWS, int STEP>
+__device__ __forceinline__ void make_job(const AttnParams& p, int b, int item, int step, int64_t s, int64_t end, Job* j) {
+  Span x = span<ROWS, STEP>(p, b);
+  while (item >= x.items && b + 1 < p.B) {     // the first sequence from here on that has rows: one exists, as s < end
+    item = 0;
+    x = span<ROWS, STEP>(p, ++b);
+  }
+  j->x = x;
+  j->b = b;
+  j->item = item;
+  j->step = step;
+  j->steps = static_cast<int>(min(static_cast<int64_t>(x.steps - step), end - s));
+  j->key = x.lo + step * STEP;
+  j->s = s;
+}
 
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -195,6 +201,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum: no accumulator to read.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // A power of two that brings a value of magnitude amax to [2^14, 2^15) (as far
 // as fp32 has it), by its exponent k.
 __device__ __forceinline__ int row_exponent(float amax) {
@@ -204,10 +220,9 @@ __device__ __forceinline__ int row_exponent(float amax) {
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
 template <int D, int NT, int WARPS, int CTAS>
-__global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(AttnParams p) {
+__global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __grid_constant__ AttnParams p) {
   using L = Layout<D, NT, WARPS>;
   constexpr int kRows = L::kRows, kStep = L::kStep, kSteps = D / 16;
-  using Where = Place<kRows, kStep>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = lane_id(), warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -215,6 +230,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(AttnParams 
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
   uint2* qs = reinterpret_cast<uint2*>(smem + L::kQ);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars) + warp * kStages;
+  Job* jobs = reinterpret_cast<Job*>(smem + L::kJobs);             // two: the current one and its successor
   int64_t* misc = reinterpret_cast<int64_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<int*>(smem + L::kMisc + 96);
   if (threadIdx.x == 0) *abort = 0;
@@ -257,8 +273,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(AttnParams 
   Range range;
   range.q = total / gridDim.x;
   range.r = total - range.q * gridDim.x;
-  const int64_t begin = range.begin(blockIdx.x);
-  const int64_t end = range.begin(blockIdx.x + 1);
+  const int64_t begin = range.begin(blockIdx.x), end = range.begin(blockIdx.x + 1);
   if (begin == end) return;
   {
     int64_t ahead = 0;
@@ -266,182 +281,165 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(AttnParams 
       const int64_t all = p.B <= L::kThreads ? total : scan(base);
       if (begin >= ahead && begin < ahead + all) {
         const int64_t at = begin - ahead - before;
-        __syncthreads();
         if (at >= 0 && at < mine) {
-          misc[8] = base + threadIdx.x;
-          misc[9] = at;
+          const int b = base + static_cast<int>(threadIdx.x);
+          const int steps = span<kRows, kStep>(p, b).steps;
+          const int item = static_cast<int>(at / steps);
+          make_job<kRows, kStep>(p, b, item, static_cast<int>(at - static_cast<int64_t>(item) * steps), begin, end, jobs);
         }
-        __syncthreads();
         break;
       }
       ahead += all;
     }
   }
-  Where cur;
-  cur.b = static_cast<int>(misc[8]);
-  cur.x = span<kRows, kStep>(p, cur.b);
-  {
-    const int64_t at = misc[9];
-    cur.item = static_cast<int>(at / cur.x.steps);
-    cur.step = static_cast<int>(at - static_cast<int64_t>(cur.item) * cur.x.steps);
-  }
+  __syncthreads();
 
-  // ---- loads: the warp's tile of a step, from up to two pages ----
-  const int chunk = min(p.c.page_size, kTile), chunks = kTile / chunk;
+  // ---- loads: the warp's tile of a step, from one or two pages ----
   const uint64_t policy = policy_evict_first();
-  int pending = 0;                                  // stages with copies in flight
+  const int chunk = min(p.c.page_size, kTile);
+  const bool two = chunk < kTile;
   uint8_t* stages = smem + warp * kStages * L::kStageBytes;
+  int pending = 0;                                  // stages with copies in flight
+  // lanes 0 .. 3 (0 .. 7 where a tile spans two pages): one part each of a page's K codes, K scales, V codes, V scales
+  const int lane_key = (lane >> 2) * chunk;
+  const bool loads = lane < (two ? 8 : 4);
+  const uint8_t* lane_base = (lane & 2) ? p.c.v : p.c.k;
+  const int lane_row = (lane & 1) ? D / 16 : D / 2; // bytes of a row of this lane's part
+  uint8_t* lane_dst = stages + ((lane & 2) ? L::kCodes + L::kScales : 0) + ((lane & 1) ? L::kCodes : 0) + lane_key * lane_row;
+  if (lane & 1) lane_base += p.c.page_size * (D / 2);
   const int64_t slab = p.c.slab();
-  auto tile_of = [&](const Where& w) { return w.x.lo + w.step * kStep + warp * kTile; };
-  // this lane's page of a tile (lanes 0 .. 4 * chunks - 1: a chunk's four parts)
-  auto page_of = [&](const Where& w) {
-    const int key = tile_of(w) + (lane >> 2) * chunk;
-    int page = 0;
-    if (lane < 4 * chunks && key < w.x.hi && key + chunk > w.x.first)
-      page = p.table[w.b * p.table_stride + (key >> p.c.page_shift)];
-    return page;
+  auto page_of = [&](const int32_t* row, int key, int lo, int hi) {
+    key += lane_key;
+    return loads && key < hi && key + chunk > lo ? row[key >> p.c.page_shift] : 0;
   };
-  auto issue = [&](const Where& w, int page, int stage) {
-    const int k0 = tile_of(w);
-    if (k0 >= w.x.hi || *abort) return;
-    // of a first tile, 16-key pages ahead of the first key are left out; of a last one, those behind the last key
-    const int c0 = chunks == 2 && w.x.first >= k0 + chunk ? 1 : 0;
-    const int c1 = chunks == 2 && w.x.hi <= k0 + chunk ? 1 : chunks;
-    if (lane == 0) mbar_arrive_expect_tx(&bars[stage], (c1 - c0) * chunk * (D * 9 / 8));
+  auto issue = [&](int head, int page, int key, int lo, int hi, int stage) {
+    if (key >= hi || *abort) return;
+    // 16-key pages of a first tile that lie ahead of the first key are left out, and those of a last one behind the last
+    const bool skip0 = two && lo >= key + chunk, skip1 = two && hi <= key + chunk;
+    if (lane == 0)
+      mbar_arrive_expect_tx(&bars[stage], (skip0 || skip1 ? chunk : kTile) * (D * 9 / 8));
     __syncwarp();
     pending |= 1 << stage;
-    const int c = lane >> 2, part = lane & 3;
-    if (c >= c0 && c < c1) {
+    if (loads && !(lane < 4 ? skip0 : skip1)) {
       if (page < 0 || page >= p.c.pages) {
         atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadPage));
         page = 0;
       }
-      const int row = (k0 + c * chunk) & (p.c.page_size - 1);
-      const int head = w.item % p.c.heads;
-      const uint8_t* src = ((part & 2) ? p.c.v : p.c.k) + (static_cast<int64_t>(page) * p.c.heads + head) * slab;
-      uint8_t* dst = stages + stage * L::kStageBytes + ((part & 2) ? L::kCodes + L::kScales : 0);
-      if (part & 1)
-        bulk_load(dst + L::kCodes + c * chunk * (D / 16), src + p.c.page_size * (D / 2) + row * (D / 16),
-                  chunk * (D / 16), &bars[stage], policy);
-      else
-        bulk_load(dst + c * chunk * (D / 2), src + row * (D / 2), chunk * (D / 2), &bars[stage],
-                  policy);
+      bulk_load(lane_dst + stage * L::kStageBytes,
+                lane_base + (static_cast<int64_t>(page) * p.c.heads + head) * slab +
+                    ((key + lane_key) & (p.c.page_size - 1)) * lane_row,
+                chunk * lane_row, &bars[stage], policy);
     }
   };
-
-  // ---- the walk ----
-  Where ahead = cur;
-  int64_t s_ahead = begin;
-  int next_page = page_of(ahead);
-  int phase = 0, stage_in = 0, stage_out = 0;      // bit i of phase: stage i's parity
-  auto advance = [&]() {                            // issue the next step's tile, look its successor's page up
-    if (s_ahead >= end) return;
-    issue(ahead, next_page, stage_in);
-    stage_in ^= 1;
-    if (++s_ahead < end) {
-      ahead.next(p);
-      next_page = page_of(ahead);
-    }
-  };
-  advance();
 
   uint32_t qf[NT == 4 ? 1 : NT][kSteps][2];
-  float qscale[NT][2];
-  int first[NT][2], last[NT][2];
-  float m[NT][2], l[NT][2];
+  float qscale[NT][2], m[NT][2], l[NT][2];
+  int pos[NT][2];
   float o[kSteps][NT][4];
-  int all_first = 0, all_last = 0;                  // keys that every row of the item sees
-  bool fresh = true;
-  const int64_t seg_first = begin;
-  int64_t seg = begin;                              // first step of the current segment
+  int phase = 0, stage = 0, which = 0;
+  {
+    const Job& j = jobs[0];
+    const int key = j.key + warp * kTile;
+    issue(j.item % p.c.heads, page_of(p.table + j.b * p.table_stride, key, j.x.first, j.x.hi), key, j.x.first, j.x.hi, 0);
+  }
 
-  for (int64_t s = begin; s < end; ++s) {
-    advance();
-    if (fresh) {
-      // the item's query rows: lane (g, t) holds row 8 nt + g, elements [t D/4, (t + 1) D/4)
-      fresh = false;
-      seg = s;
-      const int head = cur.item % p.c.heads, row0 = cur.item / p.c.heads * kRows;
-      const int rows = cur.x.s.n * p.group;
-      if constexpr (NT == 4) __syncthreads();       // the previous item's fragments are no longer read
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int r = row0 + nt * 8 + g;
-        uint32_t w[D / 8];
-        if (r < rows) {
-          const uint16_t* src = p.q + (cur.x.s.r0 + r / p.group) * p.qt + (head * p.group + r % p.group) * p.qh + t * (D / 4);
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
-            w[4 * i] = v.x;
-            w[4 * i + 1] = v.y;
-            w[4 * i + 2] = v.z;
-            w[4 * i + 3] = v.w;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) w[i] = 0;
-        }
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        const int k = row_exponent(amax);
-        const float up = pow2(k), down = pow2(-k) * p.scale;
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const uint32_t b0 = pack_f16x2(bf16lo(w[2 * i]) * up, bf16hi(w[2 * i]) * up);
-          const uint32_t b1 = pack_f16x2(bf16lo(w[2 * i + 1]) * up, bf16hi(w[2 * i + 1]) * up);
-          if constexpr (NT == 4) {
-            if (warp == 0) qs[(nt * kSteps + i) * 32 + lane] = make_uint2(b0, b1);
-          } else {
-            qf[nt][i][0] = b0;
-            qf[nt][i][1] = b1;
-          }
-        }
-        qscale[nt][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
-        qscale[nt][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = row0 + nt * 8 + 2 * t + i;
-          const int pos = cur.x.s.kv - cur.x.s.n + row / p.group;
-          first[nt][i] = visible_first(p, pos);
-          last[nt][i] = row < rows ? visible_last(p, cur.x.s, pos) : 0;
-          m[nt][i] = -INFINITY;
-          l[nt][i] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
-      }
-      all_last = visible_last(p, cur.x.s, cur.x.s.kv - cur.x.s.n + row0 / p.group);
-      all_first = visible_first(p, cur.x.s.kv - cur.x.s.n + (min(rows, row0 + kRows) - 1) / p.group);
-      if constexpr (NT == 4) __syncthreads();
+  for (;; which ^= 1) {
+    // ---- an item (or this CTA's part of it): its query rows, and the next job ----
+    const Job& job = jobs[which];
+    const bool more = job.s + job.steps < end;
+    if (more && threadIdx.x == 0) {
+      const bool whole_item = job.step + job.steps == job.x.steps;       // else this CTA's range ends here
+      make_job<kRows, kStep>(p, job.b, job.item + (whole_item ? 1 : 0), 0, job.s + job.steps, end, &jobs[which ^ 1]);
     }
-
-    const int k0 = tile_of(cur);
-    if (k0 < cur.x.hi) {
-      if (!*abort && mbar_wait(&bars[stage_out], (phase >> stage_out) & 1, abort, kErrWaitFull)) {
-        phase ^= 1 << stage_out;
-        pending &= ~(1 << stage_out);
+    const Seq seq = job.x.s;
+    const int hi = job.x.hi, lo = job.x.first, steps = job.steps, item = job.item;
+    const int head = item % p.c.heads, row0 = item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
+    const int32_t* table = p.table + job.b * p.table_stride;
+    int key = job.key + warp * kTile;
+    int page = steps > 1 ? page_of(table, key + kStep, lo, hi) : 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      // lane (g, t) holds row 8 nt + g, elements [t D/4, (t + 1) D/4)
+      const int r = nt * 8 + g;
+      uint32_t w[D / 8];
+      if (r < rows) {
+        const uint16_t* src = p.q + (seq.r0 + (row0 + r) / p.group) * p.qt +
+                              (head * p.group + (row0 + r) % p.group) * p.qh + t * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = 0;
       }
-      const uint8_t* kc = stages + stage_out * L::kStageBytes;
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      const int k = row_exponent(amax);
+      const float up = pow2(k), down = pow2(-k) * p.scale;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const uint32_t b0 = pack_f16x2(bf16lo(w[2 * i]) * up, bf16hi(w[2 * i]) * up);
+        const uint32_t b1 = pack_f16x2(bf16lo(w[2 * i + 1]) * up, bf16hi(w[2 * i + 1]) * up);
+        if constexpr (NT == 4) {
+          if (warp == nt % WARPS) qs[(nt * kSteps + i) * 32 + lane] = make_uint2(b0, b1);
+        } else {
+          qf[nt][i][0] = b0;
+          qf[nt][i][1] = b1;
+        }
+      }
+      qscale[nt][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
+      qscale[nt][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        pos[nt][i] = seq.kv - seq.n + (row0 + min(nt * 8 + 2 * t + i, rows - 1)) / p.group;
+        m[nt][i] = -INFINITY;
+        l[nt][i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+    }
+    // keys that every row of the item sees
+    const int all_last = visible_last(p, seq, seq.kv - seq.n + row0 / p.group);
+    const int all_first = visible_first(p, seq.kv - seq.n + (row0 + rows - 1) / p.group);
+    __syncthreads();                                // jobs[which ^ 1] and the fragments are written
+
+    for (int i = 0; i < steps; ++i, key += kStep, stage ^= 1) {
+      // ---- the next step's tile goes on its way ----
+      if (i + 1 < steps) {
+        issue(head, page, key + kStep, lo, hi, stage ^ 1);
+        if (i + 2 < steps) page = page_of(table, key + 2 * kStep, lo, hi);
+      } else if (more) {
+        const Job& j = jobs[which ^ 1];
+        const int k = j.key + warp * kTile;
+        issue(j.item % p.c.heads, page_of(p.table + j.b * p.table_stride, k, j.x.first, j.x.hi), k, j.x.first, j.x.hi,
+              stage ^ 1);
+      }
+      if (key >= hi) continue;
+      if (!*abort && mbar_wait(&bars[stage], (phase >> stage) & 1, abort, kErrWaitFull)) {
+        phase ^= 1 << stage;
+        pending &= ~(1 << stage);
+      }
+      const uint8_t* kc = stages + stage * L::kStageBytes;
       const uint8_t* ks = kc + L::kCodes;
       const uint8_t* vc = ks + L::kScales;
       const uint8_t* vs = vc + L::kCodes;
-      const bool whole = k0 >= all_first && k0 + kTile <= all_last;
+      const bool whole = key >= all_first && key + kTile <= all_last;
       // Row r of a 16-key tile is key r ^ (r / 4 & 1): K's rows of neighbouring lane groups and V's rows 2t (and
       // 2t + 1) of the four t then lie in different banks (V: at most two lanes to a bank).
       const int kg = g ^ ((g >> 2) & 1);
       float sc[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[mt][nt][i] = 0.0f;
         const int r0 = mt * 16 + kg, r1 = r0 + 8;
         uint32_t w0[D / 32], w1[D / 32], s0[2], s1[2];
         if constexpr (D == 128) {
@@ -485,52 +483,56 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(AttnParams 
                 b0 = qf[nt][2 * w + h][0];
                 b1 = qf[nt][2 * w + h][1];
               }
-              mma16816(sc[mt][nt], a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1], b0, b1);
+              if (w == 0 && h == 0) mma16816_first(sc[mt][nt], a[0], b[0], a[1], b[1], b0, b1);
+              else mma16816(sc[mt][nt], a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1], b0, b1);
             }
         }
       }
-      // softmax over the tile: element i of sc is key (g, g + 8)[i / 2], row 2t + i % 2
+      // Softmax over the tile: element i of sc is key (g, g + 8)[i / 2], row 2t + i % 2.  The base m is raised only
+      // when a score passes it by 2^8 (P, at most 256, keeps its precision in f16, and a sum of fp32 its own).
+      if (!whole) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int first = visible_first(p, pos[nt][q]), last = visible_last(p, seq, pos[nt][q]);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int k = key + mt * 16 + kg + h * 8;
+                if (k < first || k >= last) sc[mt][nt][2 * h + q] = -INFINITY;
+              }
+          }
+      }
       uint32_t pf[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float top[2] = {-INFINITY, -INFINITY};
+        float top[2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = sc[mt][nt][i] * qscale[nt][i & 1];
-            if (!whole) {
-              const int key = k0 + mt * 16 + kg + (i >> 1) * 8;
-              v = key >= first[nt][i & 1] && key < last[nt][i & 1] ? v : -INFINITY;
-            }
-            sc[mt][nt][i] = v;
-            top[i & 1] = fmaxf(top[i & 1], v);
-          }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int d = 4; d < 32; d *= 2) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], d));
-          top[i] = fmaxf(top[i], m[nt][i]);
-        }
-        if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] || top[1] > m[nt][1])) {
-          float f[2];
+        for (int i = 0; i < 2; ++i)
+          top[i] = fmaxf(fmaxf(sc[0][nt][i], sc[0][nt][i + 2]), fmaxf(sc[1][nt][i], sc[1][nt][i + 2])) * qscale[nt][i];
+        if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] + kSlack || top[1] > m[nt][1] + kSlack)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            f[i] = top[i] > m[nt][i] ? ex2(m[nt][i] - top[i]) : 1.0f;      // 0 from -infinity
-            l[nt][i] *= f[i];
-            m[nt][i] = top[i];
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], d));
+            const float f = top[i] > m[nt][i] ? ex2(m[nt][i] - top[i]) : 1.0f;      // 0 from -infinity
+            m[nt][i] = fmaxf(m[nt][i], top[i]);
+            l[nt][i] *= f;
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d) {
+              o[d][nt][i] *= f;
+              o[d][nt][i + 2] *= f;
+            }
           }
-#pragma unroll
-          for (int d = 0; d < kSteps; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[d][nt][i] *= f[i & 1];
         }
         const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            sc[mt][nt][i] = ex2(sc[mt][nt][i] - base[i & 1]);
+            sc[mt][nt][i] = ex2(fmaf(sc[mt][nt][i], qscale[nt][i & 1], -base[i & 1]));
             l[nt][i & 1] += sc[mt][nt][i];
           }
           pf[mt][nt][0] = transpose8x8(pack_f16x2(sc[mt][nt][0], sc[mt][nt][1]));
@@ -540,25 +542,26 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(AttnParams 
       // V^T: row g (and g + 8) of m-tile i is element g D/8 + 2i (and + 1); columns 2t, 2t + 1 (and + 8) are keys
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        int key[4];
-        key[0] = mt * 16 + (2 * t ^ (t >> 1));
-        key[1] = mt * 16 + ((2 * t + 1) ^ (t >> 1));
-        key[2] = key[0] + 8;
-        key[3] = key[1] + 8;
+        const int ka = mt * 16 + (2 * t ^ (t >> 1)), kb = mt * 16 + ((2 * t + 1) ^ (t >> 1));
+        const int keys[4] = {ka, kb, ka + 8, kb + 8};
         uint32_t vw[4][D / 64], sv[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (D == 128) {
-            const uint2 a = *reinterpret_cast<const uint2*>(vc + key[i] * 64 + g * 8);
+            const uint2 a = *reinterpret_cast<const uint2*>(vc + keys[i] * 64 + g * 8);
             vw[i][0] = a.x;
             vw[i][1] = a.y;
-            sv[i] = vs[key[i] * 8 + g];
+            sv[i] = vs[keys[i] * 8 + g];
           } else {
-            vw[i][0] = *reinterpret_cast<const uint32_t*>(vc + key[i] * 32 + g * 4);
-            sv[i] = vs[key[i] * 4 + (g >> 1)];
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(vc + keys[i] * 32 + g * 4);
+            sv[i] = vs[keys[i] * 4 + (g >> 1)];
           }
-          // what lies outside the keys, or was not loaded, need not be a number that times zero is zero
-          if (!whole && (k0 + key[i] >= cur.x.hi || k0 + key[i] < cur.x.first)) sv[i] = 0;
+        }
+        // what lies outside the keys, or was not loaded, need not be a number that times zero is zero
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key + keys[i] >= hi || key + keys[i] < lo) sv[i] = 0;
         }
         const uint32_t s01 = widen_e4m3x2(sv[0] | (sv[1] << 8)), s23 = widen_e4m3x2(sv[2] | (sv[3] << 8));
 #pragma unroll
@@ -582,115 +585,139 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(AttnParams 
       }
       __syncwarp();                                 // every lane has read the stage before it is filled again
     }
-    stage_out ^= 1;
 
-    // ---- the end of the item, or of the CTA's range ----
-    const bool item_ends = cur.step + 1 == cur.x.steps;
-    if (item_ends || s + 1 == end) {
+    // ---- the end of the job: the warps' results joined ----
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-          for (int d = 4; d < 32; d *= 2) l[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][i], d);
-          if (g == 0) {
-            const int r = nt * 8 + 2 * t + i;
-            ml[warp * kRows + r] = m[nt][i];
-            ml[(WARPS + warp) * kRows + r] = l[nt][i];
-          }
-        }
-      __syncthreads();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int d = 4; d < 32; d *= 2) l[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][i], d);
+        if (g == 0) {
           const int r = nt * 8 + 2 * t + i;
-          float top = -INFINITY;
-          for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
-          const float f = m[nt][i] == -INFINITY ? 0.0f : ex2(m[nt][i] - top);
-          float* dst = red + (warp * kRows + r) * L::kRedStride + g * (D / 8);
+          ml[warp * kRows + r] = m[nt][i];
+          ml[(WARPS + warp) * kRows + r] = l[nt][i];
+        }
+      }
+    __syncthreads();
 #pragma unroll
-          for (int d = 0; d < kSteps; d += 2)
-            *reinterpret_cast<float4*>(dst + 2 * d) = make_float4(o[d][nt][i] * f, o[d][nt][i + 2] * f,
-                                                                  o[d + 1][nt][i] * f, o[d + 1][nt][i + 2] * f);
-        }
-      }
-      __syncthreads();
-      const int head = cur.item % p.c.heads, row0 = cur.item / p.c.heads * kRows;
-      const int rows = min(kRows, cur.x.s.n * p.group - row0);
-      const int64_t i0 = s - cur.step, i1 = i0 + cur.x.steps;     // the item's steps in the list
-      const bool split = i0 < begin || i1 > end;
-      auto finish = [&](int r, int d, float4 v, float top, float sum) {
-        const int row = row0 + r;
-        const int64_t token = cur.x.s.r0 + row / p.group;
-        const int h = head * p.group + row % p.group;
-        const float f = sum > 0.0f ? p.c.vg / sum : 0.0f;
-        uint2 w;
-        w.x = pack_bf16x2(v.x * f, v.y * f);
-        w.y = pack_bf16x2(v.z * f, v.w * f);
-        *reinterpret_cast<uint2*>(p.o + token * p.ot + h * p.oh + d) = w;
-        if (p.lse && d == 0) p.lse[token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
-      };
-      float* slot = split ? p.part + (2 * static_cast<int64_t>(blockIdx.x) + (seg == seg_first ? 0 : 1)) * L::kPart
-                          : nullptr;
-      for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
-        const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float top = -INFINITY, sum = 0.0f;
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = nt * 8 + 2 * t + i;
+        float top = -INFINITY;
         for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int w = 0; w < WARPS; ++w) {
-          const float mw = ml[w * kRows + r];
-          if (mw != -INFINITY) sum += ml[(WARPS + w) * kRows + r] * ex2(mw - top);
-          const float4 x = *reinterpret_cast<const float4*>(red + (w * kRows + r) * L::kRedStride + d);
-          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-        }
-        if (!split) {
-          finish(r, d, v, top, sum);
-        } else {
-          __stcg(reinterpret_cast<float4*>(slot + r * D + d), v);
-          if (d == 0) {
-            __stcg(slot + kRows * D + r, top);
-            __stcg(slot + kRows * (D + 1) + r, sum);
-          }
+        const float f = m[nt][i] == -INFINITY ? 0.0f : ex2(m[nt][i] - top);
+        float* dst = red + (warp * kRows + r) * L::kRedStride + g * (D / 8);
+#pragma unroll
+        for (int d = 0; d < kSteps; d += 2)
+          *reinterpret_cast<float4*>(dst + 2 * d) = make_float4(o[d][nt][i] * f, o[d][nt][i + 2] * f,
+                                                                o[d + 1][nt][i] * f, o[d + 1][nt][i + 2] * f);
+      }
+    }
+    __syncthreads();
+    const int64_t i0 = job.s - job.step, i1 = i0 + job.x.steps;      // the item's steps in the list
+    const bool split = i0 < begin || i1 > end;
+    auto finish = [&](int r, int d, float4 v, float top, float sum) {
+      const int row = row0 + r;
+      const int64_t token = seq.r0 + row / p.group;
+      const int h = head * p.group + row % p.group;
+      const float f = sum > 0.0f ? p.c.vg / sum : 0.0f;
+      uint2 w;
+      w.x = pack_bf16x2(v.x * f, v.y * f);
+      w.y = pack_bf16x2(v.z * f, v.w * f);
+      *reinterpret_cast<uint2*>(p.o + token * p.ot + h * p.oh + d) = w;
+      if (p.lse && d == 0) p.lse[token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    };
+    float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.s == begin ? 0 : 1)) * L::kPart;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float top = -INFINITY, sum = 0.0f;
+      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int w = 0; w < WARPS; ++w) {
+        const float mw = ml[w * kRows + r];
+        if (mw != -INFINITY) sum += ml[(WARPS + w) * kRows + r] * ex2(mw - top);
+        const float4 x = *reinterpret_cast<const float4*>(red + (w * kRows + r) * L::kRedStride + d);
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+      }
+      if (!split) {
+        finish(r, d, v, top, sum);
+      } else {
+        __stcg(reinterpret_cast<float4*>(slot + r * D + d), v);
+        if (d == 0) {
+          __stcg(slot + kRows * D + r, top);
+          __stcg(slot + kRows * (D + 1) + r, sum);
         }
       }
-      if (split) {
-        const int c0 = range.owner(i0), c1 = range.owner(i1 - 1);
-        unsigned* count = p.count + (static_cast<int64_t>(cur.b) * p.row_tiles) * p.c.heads + cur.item;
+    }
+    if (split) {
+      // the last of the item's CTAs to get here joins their parts in CTA order and leaves the workspace zero
+      const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
+      unsigned* count = p.count + (static_cast<int64_t>(job.b) * p.row_tiles) * p.c.heads + item;
+      float* at0 = p.part + (2 * static_cast<int64_t>(c0) + (range.begin(c0) != i0 ? 1 : 0)) * L::kPart;
+      float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) misc[10] = atom_add_acq_rel_gpu(count, 1u);
+      __syncthreads();
+      if (static_cast<int>(misc[10]) == parts - 1) {
         __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) misc[10] = atom_add_acq_rel_gpu(count, 1u);
-        __syncthreads();
-        if (static_cast<int>(misc[10]) == c1 - c0) {              // every other part is in
-          __threadfence();
-          for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
-            const int r = i / (D / 4), d = i % (D / 4) * 4;
-            float top = -INFINITY, sum = 0.0f;
-            auto part = [&](int c) { return p.part + (2 * static_cast<int64_t>(c) + (c == c0 && range.begin(c0) != i0 ? 1 : 0)) * L::kPart; };
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part(c) + kRows * D + r));
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int c = c0; c <= c1; ++c) {
-              float* src = part(c);
-              const float mw = __ldcg(src + kRows * D + r);
-              const float f = mw == -INFINITY ? 0.0f : ex2(mw - top);
-              sum += __ldcg(src + kRows * (D + 1) + r) * f;
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
-              v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
-            }
-            finish(r, d, v, top, sum);
+        // Per part a factor exp2(m_c - m), in shared memory (as many parts at a time as fit); then the sums.
+        constexpr int kMost = WARPS * L::kRedStride;                 // parts: kMost * kRows floats fit `red`
+        float4 acc[kRows * (D / 4) / L::kThreads];
+        float tops[kRows * (D / 4) / L::kThreads], sums[kRows * (D / 4) / L::kThreads];
+#pragma unroll
+        for (int u = 0; u < kRows * (D / 4) / L::kThreads; ++u) {
+          acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          tops[u] = -INFINITY;
+          sums[u] = 0.0f;
+        }
+        for (int p0 = 0; p0 < parts; p0 += kMost / 2) {
+          const int np = min(parts - p0, kMost / 2);
+          __syncthreads();
+          for (int i = threadIdx.x; i < np * kRows; i += L::kThreads) {
+            const int c = p0 + i / kRows, r = i % kRows;
+            float* src = (c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart) + kRows * D + r;
+            red[2 * i] = __ldcg(src);
+            red[2 * i + 1] = __ldcg(src + kRows);
+            __stcg(src, 0.0f);
+            __stcg(src + kRows, 0.0f);
           }
           __syncthreads();
-          for (int c = c0; c <= c1; ++c) {                        // the workspace is left all zero
-            float* dst = p.part + (2 * static_cast<int64_t>(c) + (c == c0 && range.begin(c0) != i0 ? 1 : 0)) * L::kPart;
-            for (int i = threadIdx.x; i < L::kPart; i += L::kThreads) __stcg(dst + i, 0.0f);
+#pragma unroll
+          for (int u = 0; u < kRows * (D / 4) / L::kThreads; ++u) {
+            const int i = threadIdx.x + u * L::kThreads, r = i / (D / 4);
+            if (r >= rows) continue;
+            float top = tops[u];
+            for (int c = 0; c < np; ++c) top = fmaxf(top, red[2 * (c * kRows + r)]);
+            const float f0 = tops[u] == -INFINITY ? 0.0f : ex2(tops[u] - top);
+            acc[u].x *= f0; acc[u].y *= f0; acc[u].z *= f0; acc[u].w *= f0;
+            sums[u] *= f0;
+            tops[u] = top;
+#pragma unroll 8
+            for (int c = 0; c < np; ++c) {
+              float4* src = reinterpret_cast<float4*>(p0 + c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(p0 + c - 1) * L::kPart) + i;
+              const float4 x = __ldcg(src);
+              const float mc = red[2 * (c * kRows + r)], f = mc == -INFINITY ? 0.0f : ex2(mc - top);
+              sums[u] += red[2 * (c * kRows + r) + 1] * f;
+              acc[u].x += x.x * f; acc[u].y += x.y * f; acc[u].z += x.z * f; acc[u].w += x.w * f;
+            }
+            for (int c = 0; c < np; ++c)
+              __stcg(reinterpret_cast<float4*>(p0 + c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(p0 + c - 1) * L::kPart) + i,
+                     make_float4(0.0f, 0.0f, 0.0f, 0.0f));
           }
-          if (threadIdx.x == 0) *count = 0;
         }
+#pragma unroll
+        for (int u = 0; u < kRows * (D / 4) / L::kThreads; ++u) {
+          const int i = threadIdx.x + u * L::kThreads, r = i / (D / 4);
+          if (r < rows) finish(r, i % (D / 4) * 4, acc[u], tops[u], sums[u]);
+        }
+        if (threadIdx.x == 0) *count = 0;
       }
-      fresh = true;
-      __syncthreads();                              // red, ml and misc are free again
     }
-    cur.next(p);
+    if (!more) break;
+    __syncthreads();                                // red, ml, misc and jobs[which] are free again
   }
   // A wait that ran out: the copies still in flight land before the shared memory is given back.
   if (*abort)
