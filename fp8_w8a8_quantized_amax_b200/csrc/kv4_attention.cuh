@@ -222,6 +222,7 @@ template <int D, int NT, int WARPS, int CTAS>
 __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __grid_constant__ AttnParams p) {
   using L = Layout<D, NT, WARPS>;
   constexpr int kRows = L::kRows, kStep = L::kStep, kSteps = D / 16;
+  constexpr int kHalves = NT == 4 ? 1 : 2;          // 16-key halves of a tile worked on together (registers)
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = lane_id(), warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -289,59 +290,59 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
   // Nine 16-byte copies a lane at D = 128: four of K's codes, four of V's, one of the scales (lanes 0 .. 15 K's, the
   // others V's).  Bulk copies would need one instruction per run, issued lane by lane: with four runs a tile they
   // took as many issue slots as the products (measured: 95 us against 75 us on 64 ragged sequences of up to 8192 keys).
-  const bool two = p.c.page_size < kTile;
   uint8_t* stages = smem + warp * kStages * L::kStageBytes;
-  const int64_t slab = p.c.slab();
-  const int scale_at = p.c.page_size * (D / 2);
+  const uint32_t slab = static_cast<uint32_t>(p.c.slab()), page_bytes = slab * p.c.heads;
   constexpr int kLoads = L::kCodes / 512;           // 16-byte copies a lane for one tensor's codes
   constexpr int kScaleLanes = L::kScales / 16;      // lanes that copy one tensor's scales
-  // pages of a tile's two halves (page 0 stands for one that no key needs: what is read there is masked)
+  const int scale_key = lane % kScaleLanes * (256 / D);                 // first key of this lane's 16 bytes of scales
+  const int64_t v_from_k = p.c.v - p.c.k;
+  // what this lane's copies start from: K's codes (and the scales, of K or V) of an item's head
+  auto codes_of = [&](int head) { return p.c.k + static_cast<int64_t>(head) * slab + lane * 16; };
+  auto scales_of = [&](int head) {
+    return (lane < kScaleLanes ? p.c.k : p.c.v) + static_cast<int64_t>(head) * slab + p.c.page_size * (D / 2);
+  };
+  // Pages of a tile's two halves (one page, where pages hold 32 keys or more).  A half that no key needs is stood in
+  // for by the nearest that one does: what is read there is masked.
   auto pages_of = [&](const int32_t* row, int key, int lo, int hi) {
-    int2 v = make_int2(0, 0);
-    if (key < hi && (!two || key + kTile / 2 > lo)) v.x = row[key >> p.c.page_shift];
-    if (!two) v.y = v.x;
-    else if (key + kTile / 2 < hi) v.y = row[(key + kTile / 2) >> p.c.page_shift];
+    int2 v;
+    v.x = row[min(max(key, lo), hi - 1) >> p.c.page_shift];
+    v.y = row[min(max(key + kTile / 2, lo), hi - 1) >> p.c.page_shift];
     return v;
   };
-  auto issue = [&](int head, int2 page, int key, int hi, int stage) {
-    if (key < hi) {
-      if (static_cast<unsigned>(page.x) >= static_cast<unsigned>(p.c.pages) ||
-          static_cast<unsigned>(page.y) >= static_cast<unsigned>(p.c.pages)) {
-        atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadPage));
-        page = make_int2(0, 0);
-      }
-      uint8_t* dst = stages + stage * L::kStageBytes;
-      const int row = key & (p.c.page_size - 1);
-      const int64_t offx = (static_cast<int64_t>(page.x) * p.c.heads + head) * slab + row * (D / 2) + lane * 16;
-      const int64_t offy = two ? (static_cast<int64_t>(page.y) * p.c.heads + head) * slab - (kTile / 2) * (D / 2) + lane * 16
-                               : offx;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int64_t off = (i < kLoads / 2 ? offx : offy) + i * 512;
-        cp_async_16(dst + i * 512 + lane * 16, p.c.k + off);
-        cp_async_16(dst + L::kCodes + L::kScales + i * 512 + lane * 16, p.c.v + off);
-      }
-      if (lane < 2 * kScaleLanes) {
-        const int u = lane % kScaleLanes;             // of the tensor's scale rows: 16 bytes each
-        const bool second = two && u >= kScaleLanes / 2;
-        const int64_t off = (static_cast<int64_t>(second ? page.y : page.x) * p.c.heads + head) * slab + scale_at +
-                            (two ? (u % (kScaleLanes / 2)) * 16 : row * (D / 16) + u * 16);
-        cp_async_16(dst + L::kCodes + u * 16 + (lane < kScaleLanes ? 0 : L::kCodes + L::kScales),
-                    (lane < kScaleLanes ? p.c.k : p.c.v) + off);
-      }
+  auto issue = [&](const uint8_t* codes, const uint8_t* scales, int2 page, int key, int stage) {
+    if (static_cast<unsigned>(max(page.x, page.y)) >= static_cast<unsigned>(p.c.pages) || min(page.x, page.y) < 0) {
+      atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadPage));
+      page = make_int2(0, 0);
     }
-    cp_async_commit();                                // one group a step, empty or not
+    uint8_t* dst = stages + stage * L::kStageBytes + lane * 16;
+    const int in_page = p.c.page_size - 1;
+    const uint8_t* src[2];
+    src[0] = codes + static_cast<uint64_t>(static_cast<uint32_t>(page.x)) * page_bytes + (key & in_page) * (D / 2);
+    src[1] = codes + static_cast<uint64_t>(static_cast<uint32_t>(page.y)) * page_bytes + ((key + kTile / 2) & in_page) * (D / 2);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint8_t* from = src[i / (kLoads / 2)] + i % (kLoads / 2) * 512;
+      cp_async_16(dst + i * 512, from);
+      cp_async_16(dst + L::kCodes + L::kScales + i * 512, from + v_from_k);
+    }
+    if (lane < 2 * kScaleLanes)
+      cp_async_16(dst + L::kCodes + (lane < kScaleLanes ? 0 : L::kCodes),
+                  scales + static_cast<uint64_t>(static_cast<uint32_t>(scale_key < kTile / 2 ? page.x : page.y)) * page_bytes +
+                      ((key + scale_key) & in_page) * (D / 16));
   };
 
   uint32_t qf[NT == 4 ? 1 : NT][kSteps][2];
-  float qscale[NT][2], m[NT][2], l[NT][2];
+  // per row: the scores' factor, the base m (negated; 0 before the first key), the score at which it is raised, the sum
+  float qscale[NT][2], nbase[NT][2], limit[NT][2], l[NT][2];
   int pos[NT][2];
   float o[kSteps][NT][4];
   int stage = 0, which = 0;
   {
     const Job& j = jobs[0];
-    const int key = j.key + warp * kTile;
-    issue(j.item % p.c.heads, pages_of(p.table + j.b * p.table_stride, key, j.x.first, j.x.hi), key, j.x.hi, 0);
+    const int key = j.key + warp * kTile, head = j.item % p.c.heads;
+    if (key < j.x.hi)
+      issue(codes_of(head), scales_of(head), pages_of(p.table + j.b * p.table_stride, key, j.x.first, j.x.hi), key, 0);
+    cp_async_commit();
   }
 
   for (;; which ^= 1) {
@@ -357,7 +358,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
     const int head = item % p.c.heads, row0 = item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
     const int32_t* table = p.table + job.b * p.table_stride;
     int key = job.key + warp * kTile;
-    int2 page = steps > 1 ? pages_of(table, key + kStep, lo, hi) : make_int2(0, 0);
+    const uint8_t* codes = codes_of(head);
+    const uint8_t* scales = scales_of(head);
+    int2 page = make_int2(0, 0);
+    if (key + kStep < hi) page = pages_of(table, key + kStep, lo, hi);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       // lane (g, t) holds row 8 nt + g, elements [t D/4, (t + 1) D/4)
@@ -401,7 +405,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         pos[nt][i] = seq.kv - seq.n + (row0 + min(nt * 8 + 2 * t + i, rows - 1)) / p.group;
-        m[nt][i] = -INFINITY;
+        nbase[nt][i] = 0.0f;
+        limit[nt][i] = -INFINITY;
         l[nt][i] = 0.0f;
       }
 #pragma unroll
@@ -417,15 +422,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
     for (int i = 0; i < steps; ++i, key += kStep, stage ^= 1) {
       // ---- the next step's tile goes on its way ----
       if (i + 1 < steps) {
-        issue(head, page, key + kStep, hi, stage ^ 1);
-        if (i + 2 < steps) page = pages_of(table, key + 2 * kStep, lo, hi);
+        if (key + kStep < hi) issue(codes, scales, page, key + kStep, stage ^ 1);
+        if (key + 2 * kStep < hi) page = pages_of(table, key + 2 * kStep, lo, hi);
       } else if (more) {
         const Job& j = jobs[which ^ 1];
-        const int k = j.key + warp * kTile;
-        issue(j.item % p.c.heads, pages_of(p.table + j.b * p.table_stride, k, j.x.first, j.x.hi), k, j.x.hi, stage ^ 1);
-      } else {
-        cp_async_commit();
+        const int k = j.key + warp * kTile, h = j.item % p.c.heads;
+        if (k < j.x.hi)
+          issue(codes_of(h), scales_of(h), pages_of(p.table + j.b * p.table_stride, k, j.x.first, j.x.hi), k, stage ^ 1);
       }
+      cp_async_commit();                            // one group a step, empty or not
       if (key >= hi) continue;
       cp_async_wait<1>();
       __syncwarp();                                 // the other lanes' copies too
@@ -437,10 +442,12 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       // Row r of a 16-key tile is key r ^ (r / 4 & 1): K's rows of neighbouring lane groups and V's rows 2t (and
       // 2t + 1) of the four t then lie in different banks (V: at most two lanes to a bank).
       const int kg = g ^ ((g >> 2) & 1);
-      float sc[2][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const int r0 = mt * 16 + kg, r1 = r0 + 8;
+      for (int m0 = 0; m0 < 2; m0 += kHalves) {
+      float sc[kHalves][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < kHalves; ++mt) {
+        const int r0 = (m0 + mt) * 16 + kg, r1 = r0 + 8;
         uint32_t w0[D / 32], w1[D / 32], s0[2], s1[2];
         if constexpr (D == 128) {
           const uint4 a = *reinterpret_cast<const uint4*>(kc + r0 * 64 + t * 16);
@@ -490,59 +497,69 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       }
       // Softmax over the tile: element i of sc is key (g, g + 8)[i / 2], row 2t + i % 2.  The base m is raised only
       // when a score passes it by 2^8 (P, at most 256, keeps its precision in f16, and a sum of fp32 its own).
-      if (!whole) {
+      if (__builtin_expect(!whole, 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int first = visible_first(p, pos[nt][q]), last = visible_last(p, seq, pos[nt][q]);
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < kHalves; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int k = key + mt * 16 + kg + h * 8;
+                const int k = key + (m0 + mt) * 16 + kg + h * 8;
                 if (k < first || k >= last) sc[mt][nt][2 * h + q] = -INFINITY;
               }
           }
       }
-      uint32_t pf[2][NT][2];
+      uint32_t pf[kHalves][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float top[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          top[i] = fmaxf(fmaxf(sc[0][nt][i], sc[0][nt][i + 2]), fmaxf(sc[1][nt][i], sc[1][nt][i + 2])) * qscale[nt][i];
-        if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] + kSlack || top[1] > m[nt][1] + kSlack)) {
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(sc[0][nt][i], sc[0][nt][i + 2]);
+          if constexpr (kHalves == 2) top[i] = fmaxf(top[i], fmaxf(sc[1][nt][i], sc[1][nt][i + 2]));
+        }
+        if (__any_sync(0xFFFFFFFFu, top[0] > limit[nt][0] || top[1] > limit[nt][1])) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], d));
-            const float f = top[i] > m[nt][i] ? ex2(m[nt][i] - top[i]) : 1.0f;      // 0 from -infinity
-            m[nt][i] = fmaxf(m[nt][i], top[i]);
-            l[nt][i] *= f;
+            const float was = limit[nt][i] == -INFINITY ? -INFINITY : -nbase[nt][i];
+            const float now = fmaxf(was, top[i] * qscale[nt][i]);
+            if (now > was) {                        // (a row without a visible key so far stays at -infinity)
+              const float f = ex2(was - now);       // 0 from -infinity
+              nbase[nt][i] = -now;
+              limit[nt][i] = (now + kSlack) / qscale[nt][i];
+              l[nt][i] *= f;
 #pragma unroll
-            for (int d = 0; d < kSteps; ++d) {
-              o[d][nt][i] *= f;
-              o[d][nt][i + 2] *= f;
+              for (int d = 0; d < kSteps; ++d) {
+                o[d][nt][i] *= f;
+                o[d][nt][i + 2] *= f;
+              }
             }
           }
         }
-        const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
+        const uint64_t scale2 = f32x2_pack(qscale[nt][0], qscale[nt][1]), base2 = f32x2_pack(nbase[nt][0], nbase[nt][1]);
+        uint64_t l2 = f32x2_pack(l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < kHalves; ++mt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sc[mt][nt][i] = ex2(fmaf(sc[mt][nt][i], qscale[nt][i & 1], -base[i & 1]));
-            l[nt][i & 1] += sc[mt][nt][i];
+          for (int h = 0; h < 2; ++h) {
+            float x, y;
+            f32x2_unpack(fma_f32x2(f32x2_pack(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]), scale2, base2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            l2 = add_f32x2(l2, f32x2_pack(x, y));
+            pf[mt][nt][h] = transpose8x8(pack_f16x2(x, y));
           }
-          pf[mt][nt][0] = transpose8x8(pack_f16x2(sc[mt][nt][0], sc[mt][nt][1]));
-          pf[mt][nt][1] = transpose8x8(pack_f16x2(sc[mt][nt][2], sc[mt][nt][3]));
-        }
+        f32x2_unpack(l2, l[nt][0], l[nt][1]);
       }
       // V^T: row g (and g + 8) of m-tile i is element g D/8 + 2i (and + 1); columns 2t, 2t + 1 (and + 8) are keys
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const int ka = mt * 16 + (2 * t ^ (t >> 1)), kb = mt * 16 + ((2 * t + 1) ^ (t >> 1));
+      for (int mt = 0; mt < kHalves; ++mt) {
+        const int ka = (m0 + mt) * 16 + (2 * t ^ (t >> 1)), kb = (m0 + mt) * 16 + ((2 * t + 1) ^ (t >> 1));
         const int keys[4] = {ka, kb, ka + 8, kb + 8};
         uint32_t vw[4][D / 64], sv[4];
 #pragma unroll
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
           }
         }
         // what lies outside the keys, or was not loaded, need not be a number that times zero is zero
-        if (!whole) {
+        if (__builtin_expect(!whole, 0)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (key + keys[i] >= hi || key + keys[i] < lo) sv[i] = 0;
@@ -583,6 +600,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
           }
         }
       }
+      }
       __syncwarp();                                 // every lane has read the stage before it is filled again
     }
 
@@ -595,7 +613,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
         for (int d = 4; d < 32; d *= 2) l[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][i], d);
         if (g == 0) {
           const int r = nt * 8 + 2 * t + i;
-          ml[warp * kRows + r] = m[nt][i];
+          ml[warp * kRows + r] = limit[nt][i] == -INFINITY ? -INFINITY : -nbase[nt][i];
           ml[(WARPS + warp) * kRows + r] = l[nt][i];
         }
       }
@@ -607,7 +625,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
         const int r = nt * 8 + 2 * t + i;
         float top = -INFINITY;
         for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
-        const float f = m[nt][i] == -INFINITY ? 0.0f : ex2(m[nt][i] - top);
+        const float f = limit[nt][i] == -INFINITY ? 0.0f : ex2(-nbase[nt][i] - top);
         float* dst = red + (warp * kRows + r) * L::kRedStride + g * (D / 8);
 #pragma unroll
         for (int d = 0; d < kSteps; d += 2)
