@@ -5,6 +5,7 @@
 #include "host.cuh"
 #include "kv4.cuh"
 #include "kv4_attention.cuh"
+#include "kv4_prefill.cuh"
 #include "rope.cuh"
 
 // The device error word of this file's kernels (fp8q_device_error reads it).
@@ -72,23 +73,38 @@ fp8q_status check_rows(const void* p, int64_t t, int64_t h) {
   return FP8Q_OK;
 }
 
-// What a call of these sizes launches: 8 nt rows a tile, `ctas` of them, and
-// the workspace: an arrival counter for each item, then two partial results per CTA.
+// What a call of these sizes launches: the kernel for few rows with 8 nt rows a
+// tile, or (nt = 0) the one for many; `ctas` CTAs; and the workspace: a header
+// of arrival counters, one per CTA, then two partial results per CTA.
+constexpr size_t kWorkspaceHeader = 4096;
+static_assert(kWorkspaceHeader == FP8Q_KV4_WORKSPACE_HEADER, "as declared");
+
 struct AttentionPlan {
   int nt, ctas, row_tiles;
-  size_t counters, part;
-  size_t bytes() const { return counters + static_cast<size_t>(2 * ctas) * part; }
+  size_t part;
+  size_t bytes() const { return kWorkspaceHeader + static_cast<size_t>(2 * ctas) * part; }
 };
 
-AttentionPlan attention_plan(const fp8q_kv4_cache* c, int64_t B, int64_t T, int64_t Hq, int64_t max_q_len, int sms) {
+AttentionPlan attention_plan(const fp8q_kv4_cache* c, int64_t T, int64_t Hq, int64_t max_q_len, int sms) {
   const int64_t rows = (max_q_len < T ? max_q_len : T) * (Hq / c->kv_heads);
   AttentionPlan a;
-  a.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
-  a.ctas = sms * (a.nt == 1 ? 4 : (a.nt == 2 ? 3 : 2));
-  a.row_tiles = static_cast<int>((rows + 8 * a.nt - 1) / (8 * a.nt));
-  a.counters = (static_cast<size_t>(B) * a.row_tiles * c->kv_heads * sizeof(unsigned) + 255) & ~size_t(255);
-  a.part = static_cast<size_t>(8 * a.nt) * (c->head_dim + 2) * sizeof(float);
+  a.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 32 ? 4 : 0));
+  a.ctas = sms * (a.nt == 1 ? 4 : (a.nt == 2 ? 3 : (a.nt == 4 ? 2 : 1)));
+  const int most = static_cast<int>(kWorkspaceHeader / (2 * sizeof(unsigned)));   // two counters a CTA at most
+  if (a.ctas > most) a.ctas = most;
+  const int64_t tile = a.nt ? 8 * a.nt : fp8q::kv4::many::kRows;
+  a.row_tiles = static_cast<int>((rows + tile - 1) / tile);
+  a.part = static_cast<size_t>(tile) * (c->head_dim + 2) * sizeof(float);
   return a;
+}
+
+template <int D>
+fp8q_status launch_many(const fp8q::kv4::AttnParams& p, int ctas, int dev, void* stream) {
+  using L = fp8q::kv4::many::Layout<D>;
+  auto k = fp8q::kv4::many::attention_kernel<D>;
+  fp8q_status st = ensure_smem(k, L::kBytes, dev);
+  if (st != FP8Q_OK) return st;
+  return launch(k, dim3(static_cast<unsigned>(ctas)), dim3(fp8q::kv4::many::kThreads), L::kBytes, stream, p);
 }
 
 template <int D, int NT, int CTAS>
@@ -279,7 +295,7 @@ size_t fp8q_kv4_attention_workspace_size(const fp8q_kv4_cache* cache, int64_t B,
   if (Hq % cache->kv_heads != 0 || T > kInt32Max || Hq > 65536 || T * Hq > kInt32Max || B > 65536) return 0;
   int dev, sms;
   if (current_device(&dev, &sms) != FP8Q_OK) return 0;
-  return attention_plan(cache, B, T, Hq, max_q_len, sms).bytes();
+  return attention_plan(cache, T, Hq, max_q_len, sms).bytes();
 }
 
 fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, int64_t q_token_stride,
@@ -330,19 +346,21 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   p.scale = sm_scale * cache->k_scale * 1.44269504088896340736f;
   p.causal = causal;
   p.window = window;
-  const AttentionPlan plan = attention_plan(cache, B, T, Hq, max_q_len, sms);
+  const AttentionPlan plan = attention_plan(cache, T, Hq, max_q_len, sms);
   if (workspace_bytes < plan.bytes()) return FP8Q_ERR_INVALID_ARG;
   p.count = static_cast<unsigned*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.counters);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
   p.row_tiles = plan.row_tiles;
   if (cache->head_dim == 128) {
     if (plan.nt == 1) return launch_few<128, 1, 4>(p, plan.ctas, dev, stream);
     if (plan.nt == 2) return launch_few<128, 2, 3>(p, plan.ctas, dev, stream);
-    return launch_few<128, 4, 2>(p, plan.ctas, dev, stream);
+    if (plan.nt == 4) return launch_few<128, 4, 2>(p, plan.ctas, dev, stream);
+    return launch_many<128>(p, plan.ctas, dev, stream);
   }
   if (plan.nt == 1) return launch_few<64, 1, 4>(p, plan.ctas, dev, stream);
   if (plan.nt == 2) return launch_few<64, 2, 3>(p, plan.ctas, dev, stream);
-  return launch_few<64, 4, 2>(p, plan.ctas, dev, stream);
+  if (plan.nt == 4) return launch_few<64, 4, 2>(p, plan.ctas, dev, stream);
+  return launch_many<64>(p, plan.ctas, dev, stream);
 }
 
 }  // extern "C"

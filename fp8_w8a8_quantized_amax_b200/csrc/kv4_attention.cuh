@@ -20,7 +20,7 @@ struct AttnParams {
   const int32_t* table;
   const int32_t* kv_len;
   const int32_t* q_start;   // nullptr: one row per sequence
-  unsigned* count;          // workspace: arrivals per (sequence, row tile, head)
+  unsigned* count;          // workspace: arrivals at the item that is cut at a CTA's end
   float* part;              // workspace: two partial results per CTA
   int64_t qt, qh, ot, oh, table_stride;
   int T, B, Hq, group, max_pages, max_q, row_tiles;
@@ -60,55 +60,7 @@ __device__ __forceinline__ int visible_last(const AttnParams& p, const Seq& s, i
   return p.causal ? max(0, min(s.kv, pos + 1)) : s.kv;
 }
 
-// ------------------------------------------------------------ few rows ---
-//
-// Up to 8 NT query rows per key head (the group's heads times the new tokens)
-// meet every cached key, so the work is the stream of the cache: 9 D / 8 bytes
-// per key and head.  Matrix instructions keep the products off the CUDA cores;
-// with at most 8 NT columns they are mma.sync m16n8k16 with the keys (then the
-// dimensions) as rows: the dequantized operand goes straight from registers
-// into the instruction, where tcgen05 would want it written back to shared
-// memory first.
-//   S^T [16 keys, 8 rows]  = K [16 keys, D] . Q^T       (A = K, dequantized)
-//   O^T [16 dims, 8 rows] += V^T [16 dims, 16 keys] . P^T  (A = V^T)
-// Both contractions may go over their index in any order as long as both
-// operands agree, so each lane takes a contiguous run of a cache row: of K's
-// rows 32 elements (one 16-byte load, two scales), of V's rows 16 (one scale).
-// V^T's operand pairs two keys in a register: the two keys' nibbles are merged
-// into bytes (two logic operations for four values) before they are widened.
-// E2M1 times E4M3 is exact in f16.  Q is scaled by a power of two per row so
-// that its bf16 values are f16 values (all of them that are not below 2^-38 of
-// the row's largest); P, at most 1, is rounded to f16.
-//
-// The keys of a (sequence, key head) are cut into steps of WARPS * 32; the
-// list of all steps is cut evenly over the CTAs (stream-K, as in the linear's
-// decode kernel), whatever the lengths.  A warp takes 32 keys of each step
-// through its own two-stage ring of asynchronous copies and keeps its own running
-// maximum, sum and O^T; the warps' results are joined where an item ends.  An
-// item cut between CTAs is joined by the last of them to finish, in CTA order.
-namespace few {
-
-constexpr int kTile = 32;     // keys of a warp per step
-constexpr int kStages = 2;
-constexpr float kSlack = 8.0f;
-
-template <int D, int NT, int WARPS>
-struct Layout {
-  static constexpr int kThreads = 32 * WARPS;
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kStep = WARPS * kTile;
-  static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
-  static constexpr int kStageBytes = 2 * (kCodes + kScales);       // K codes, K scales, V codes, V scales
-  static constexpr int kRedStride = D + 4;
-  static constexpr int kRed = WARPS * kStages * kStageBytes;       // [WARPS][kRows][kRedStride] fp32
-  static constexpr int kMl = kRed + WARPS * kRows * kRedStride * 4;   // [WARPS][kRows] m, then l
-  static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // NT = 4: Q fragments
-  static constexpr int kMisc = kQ + (NT == 4 ? NT * (D / 16) * 32 * 8 : 0);
-  static constexpr int kJobs = kMisc + 128;                        // two jobs of at most 64 bytes
-  static constexpr int kBytes = kJobs + 128;
-  static constexpr int kPart = kRows * (D + 2);                    // floats of a partial result
-};
-
+// The list of all steps of a call, cut evenly over the CTAs.
 struct Range {
   int64_t q, r;   // CTA c takes q + 1 steps when c < r, else q
   __device__ int64_t begin(int64_t c) const { return c * q + min(c, r); }
@@ -118,51 +70,8 @@ struct Range {
   }
 };
 
-// A sequence's keys [first, hi) that some row sees, lo (first rounded down to a
-// tile), the steps they make and the number of items (row tiles times key heads).
-struct Span {
-  Seq s;
-  int first, lo, hi, steps, items;
-};
-
-template <int ROWS, int STEP>
-__device__ __forceinline__ Span span(const AttnParams& p, int b) {
-  Span x;
-  x.s = sequence(p, b);
-  x.hi = x.s.kv;
-  x.first = visible_first(p, x.s.kv - x.s.n);
-  x.lo = x.first & ~(kTile - 1);
-  x.steps = max(1, (x.hi - x.lo + STEP - 1) / STEP);
-  x.items = x.s.n > 0 ? (x.s.n * p.group + ROWS - 1) / ROWS * p.c.heads : 0;
-  return x;
-}
-
-// A CTA's part of one item: `steps` steps from key `key` on, its number in the
-// list, and what the item is.
-struct Job {
-  Span x;
-  int b, item, step, steps, key;
-  int64_t s;                 // the part's first step in the list
-};
-static_assert(sizeof(Job) <= 64, "two of them in the layout");
-
-// The job that starts at step s of the list, in sequence b, item `item` (both
-// may be one past their end) and step `step`; the CTA's range ends at `end`.
-template <int ROWS, int STEP>
-__device__ __forceinline__ void make_job(const AttnParams& p, int b, int item, int step, int64_t s, int64_t end, Job* j) {
-  Span x = span<ROWS, STEP>(p, b);
-  while (item >= x.items && b + 1 < p.B) {     // the first sequence from here on that has rows: one exists, as s < end
-    item = 0;
-    x = span<ROWS, STEP>(p, ++b);
-  }
-  j->x = x;
-  j->b = b;
-  j->item = item;
-  j->step = step;
-  j->steps = static_cast<int>(min(static_cast<int64_t>(x.steps - step), end - s));
-  j->key = x.lo + step * STEP;
-  j->s = s;
-}
+// The softmax base is raised only when a score passes it by 2^kSlack: P, at most 256, keeps its precision in f16.
+constexpr float kSlack = 8.0f;
 
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -210,6 +119,9 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+// The scores' factor stays a normal number: minus infinity times it has to be minus infinity.
+constexpr float kLeastScale = 1.17549435e-38f;
+
 // A power of two that brings a value of magnitude amax to [2^14, 2^15) (as far
 // as fp32 has it), by its exponent k.
 __device__ __forceinline__ int row_exponent(float amax) {
@@ -217,6 +129,100 @@ __device__ __forceinline__ int row_exponent(float amax) {
   return amax > 0.0f ? min(126, 141 - e) : 0;
 }
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
+
+// ------------------------------------------------------------ few rows ---
+//
+// Up to 8 NT query rows per key head (the group's heads times the new tokens)
+// meet every cached key, so the work is the stream of the cache: 9 D / 8 bytes
+// per key and head.  Matrix instructions keep the products off the CUDA cores;
+// with at most 8 NT columns they are mma.sync m16n8k16 with the keys (then the
+// dimensions) as rows: the dequantized operand goes straight from registers
+// into the instruction, where tcgen05 would want it written back to shared
+// memory first.
+//   S^T [16 keys, 8 rows]  = K [16 keys, D] . Q^T       (A = K, dequantized)
+//   O^T [16 dims, 8 rows] += V^T [16 dims, 16 keys] . P^T  (A = V^T)
+// Both contractions may go over their index in any order as long as both
+// operands agree, so each lane takes a contiguous run of a cache row: of K's
+// rows 32 elements (one 16-byte load, two scales), of V's rows 16 (one scale).
+// V^T's operand pairs two keys in a register: the two keys' nibbles are merged
+// into bytes (two logic operations for four values) before they are widened.
+// E2M1 times E4M3 is exact in f16.  Q is scaled by a power of two per row so
+// that its bf16 values are f16 values (all of them that are not below 2^-38 of
+// the row's largest); P, at most 1, is rounded to f16.
+//
+// The keys of a (sequence, key head) are cut into steps of WARPS * 32; the
+// list of all steps is cut evenly over the CTAs (stream-K, as in the linear's
+// decode kernel), whatever the lengths.  A warp takes 32 keys of each step
+// through its own two-stage ring of asynchronous copies and keeps its own running
+// maximum, sum and O^T; the warps' results are joined where an item ends.  An
+// item cut between CTAs is joined by the last of them to finish, in CTA order.
+namespace few {
+
+constexpr int kTile = 32;     // keys of a warp per step
+constexpr int kStages = 2;
+
+template <int D, int NT, int WARPS>
+struct Layout {
+  static constexpr int kThreads = 32 * WARPS;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStep = WARPS * kTile;
+  static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
+  static constexpr int kStageBytes = 2 * (kCodes + kScales);       // K codes, K scales, V codes, V scales
+  static constexpr int kRedStride = D + 4;
+  static constexpr int kRed = WARPS * kStages * kStageBytes;       // [WARPS][kRows][kRedStride] fp32
+  static constexpr int kMl = kRed + WARPS * kRows * kRedStride * 4;   // [WARPS][kRows] m, then l
+  static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // NT = 4: Q fragments
+  static constexpr int kMisc = kQ + (NT == 4 ? NT * (D / 16) * 32 * 8 : 0);
+  static constexpr int kJobs = kMisc + 128;                        // two jobs of at most 64 bytes
+  static constexpr int kBytes = kJobs + 128;
+  static constexpr int kPart = kRows * (D + 2);                    // floats of a partial result
+};
+
+// A sequence's keys [first, hi) that some row sees, lo (first rounded down to a
+// tile), the steps they make and the number of items (row tiles times key heads).
+struct Span {
+  Seq s;
+  int first, lo, hi, steps, items;
+};
+
+template <int ROWS, int STEP>
+__device__ __forceinline__ Span span(const AttnParams& p, int b) {
+  Span x;
+  x.s = sequence(p, b);
+  x.hi = x.s.kv;
+  x.first = visible_first(p, x.s.kv - x.s.n);
+  x.lo = x.first & ~(kTile - 1);
+  x.steps = max(1, (x.hi - x.lo + STEP - 1) / STEP);
+  x.items = x.s.n > 0 ? (x.s.n * p.group + ROWS - 1) / ROWS * p.c.heads : 0;
+  return x;
+}
+
+// A CTA's part of one item: `steps` steps from key `key` on, its number in the
+// list, and what the item is.
+struct Job {
+  Span x;
+  int b, item, step, steps, key;
+  int64_t s;                 // the part's first step in the list
+};
+static_assert(sizeof(Job) <= 64, "two of them in the layout");
+
+// The job that starts at step s of the list, in sequence b, item `item` (both
+// may be one past their end) and step `step`; the CTA's range ends at `end`.
+template <int ROWS, int STEP>
+__device__ __forceinline__ void make_job(const AttnParams& p, int b, int item, int step, int64_t s, int64_t end, Job* j) {
+  Span x = span<ROWS, STEP>(p, b);
+  while (item >= x.items && b + 1 < p.B) {     // the first sequence from here on that has rows: one exists, as s < end
+    item = 0;
+    x = span<ROWS, STEP>(p, ++b);
+  }
+  j->x = x;
+  j->b = b;
+  j->item = item;
+  j->step = step;
+  j->steps = static_cast<int>(min(static_cast<int64_t>(x.steps - step), end - s));
+  j->key = x.lo + step * STEP;
+  j->s = s;
+}
 
 template <int D, int NT, int WARPS, int CTAS>
 __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __grid_constant__ AttnParams p) {
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       const int k = row_exponent(amax);
-      const float up = pow2(k), down = pow2(-k) * p.scale;
+      const float up = pow2(k), down = fmaxf(pow2(-k) * p.scale, kLeastScale);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const uint32_t b0 = pack_f16x2(bf16lo(w[2 * i]) * up, bf16hi(w[2 * i]) * up);
@@ -670,9 +676,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       }
     }
     if (split) {
-      // the last of the item's CTAs to get here joins their parts in CTA order and leaves the workspace zero
+      // the last of the item's CTAs to get here joins their parts in CTA order and leaves the counter zero
       const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
-      unsigned* count = p.count + (static_cast<int64_t>(job.b) * p.row_tiles) * p.c.heads + item;
+      unsigned* count = p.count + c0;               // an item that goes on past CTA c0's end: one at most
       float* at0 = p.part + (2 * static_cast<int64_t>(c0) + (range.begin(c0) != i0 ? 1 : 0)) * L::kPart;
       float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
       __threadfence();
@@ -696,11 +702,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
           __syncthreads();
           for (int i = threadIdx.x; i < np * kRows; i += L::kThreads) {
             const int c = p0 + i / kRows, r = i % kRows;
-            float* src = (c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart) + kRows * D + r;
+            const float* src = (c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart) + kRows * D + r;
             red[2 * i] = __ldcg(src);
             red[2 * i + 1] = __ldcg(src + kRows);
-            __stcg(src, 0.0f);
-            __stcg(src + kRows, 0.0f);
           }
           __syncthreads();
 #pragma unroll
@@ -715,15 +719,12 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
             tops[u] = top;
 #pragma unroll 8
             for (int c = 0; c < np; ++c) {
-              float4* src = reinterpret_cast<float4*>(p0 + c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(p0 + c - 1) * L::kPart) + i;
+              const float4* src = reinterpret_cast<const float4*>(p0 + c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(p0 + c - 1) * L::kPart) + i;
               const float4 x = __ldcg(src);
               const float mc = red[2 * (c * kRows + r)], f = mc == -INFINITY ? 0.0f : ex2(mc - top);
               sums[u] += red[2 * (c * kRows + r) + 1] * f;
               acc[u].x += x.x * f; acc[u].y += x.y * f; acc[u].z += x.z * f; acc[u].w += x.w * f;
             }
-            for (int c = 0; c < np; ++c)
-              __stcg(reinterpret_cast<float4*>(p0 + c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(p0 + c - 1) * L::kPart) + i,
-                     make_float4(0.0f, 0.0f, 0.0f, 0.0f));
           }
         }
 #pragma unroll

@@ -442,13 +442,15 @@ FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* s
  *                   device error word.  Lengths stay on the device: a captured call
  *                   can be replayed with other lengths up to these bounds.
  *   lse             [T, Hq] fp32, written when not NULL: log sum_j exp(sm_scale q.k_j).
- *   workspace       fp8q_kv4_attention_workspace_size bytes (NULL when that is 0),
- *                   16-byte aligned, with fp8_linear's contract: zero-filled before
- *                   its first use, left all zero by every completed call, not
+ *   workspace       fp8q_kv4_attention_workspace_size bytes, 16-byte aligned.  Its first
+ *                   FP8Q_KV4_WORKSPACE_HEADER bytes are zero before its first use and left
+ *                   zero by every completed call, of any sizes; what lies behind them is
+ *                   scratch (so it is not to be shared with fp8_linear's workspace).  Not
  *                   shared by concurrent calls.
  *   A bad length or page index on the device never leads out of the tensors: it
  *   sets the device error word, and the rows concerned are not to be used.
  */
+#define FP8Q_KV4_WORKSPACE_HEADER 4096
 FP8Q_API size_t fp8q_kv4_attention_workspace_size(const fp8q_kv4_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                                   int64_t max_q_len);
 FP8Q_API fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, int64_t q_token_stride,
