@@ -16,7 +16,6 @@ activations, the FP8-Block scheme).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -398,36 +397,48 @@ class _CacheStruct(ctypes.Structure):
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
-def _on(t: torch.Tensor):
-    """The context in which a call for t's device runs: that device current."""
-    i = t.device.index
-    return contextlib.nullcontext() if i is None or i == torch.cuda.current_device() else torch.cuda.device(i)
+def _call(dev: int, name: str, *args) -> None:
+    """lib().<name>(*args, the current stream of device `dev`) with that device current; raises on an error status."""
+    f = getattr(lib(), name)
+    if dev == torch.cuda.current_device():
+        st = f(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _raw_stream(dev))
+    if st != OK:
+        raise FP8QError(st, name)
 
 
-def _require_heads(t: torch.Tensor, name: str, ref: Optional[torch.Tensor] = None, shape=None) -> None:
-    """A bf16 CUDA tensor [tokens, heads, head_dim] with contiguous elements, on ref's device."""
-    if not t.is_cuda or (ref is not None and t.device != ref.device):
-        raise ValueError(f"{name} must be a CUDA tensor" + ("" if ref is None else f" on {ref.device}"))
-    if t.dtype != torch.bfloat16:
+def _raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):      # the same handle without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _require_heads(t: torch.Tensor, name: str, dev: int, shape=None) -> None:
+    """A bf16 tensor [tokens, heads, head_dim] with contiguous elements on CUDA device `dev`."""
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{dev}" if dev >= 0 else ""))
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be bf16, got {t.dtype}")
     if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with unit stride in the last dimension")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _head_strides(t: torch.Tensor) -> Tuple[int, int]:
+def _head_strides(t: torch.Tensor, T: int, H: int, D: int) -> Tuple[int, int]:
     """(token, head) strides; those of dimensions of size 1 as in a contiguous tensor."""
-    T, H, D = t.shape
-    h = t.stride(1) if H > 1 else D
-    return (t.stride(0) if T > 1 else H * D), h
+    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
 
 
-def _require_list(t: torch.Tensor, name: str, dtype, numel: int, ref: torch.Tensor) -> None:
-    """A 1-D index or table operand: contiguous, of exactly numel elements, on ref's device."""
-    if not t.is_cuda or t.device != ref.device:
-        raise ValueError(f"{name} must be a CUDA tensor on {ref.device}")
-    if t.dtype != dtype:
+def _require_list(t: torch.Tensor, name: str, dtype, numel: int, dev: int) -> None:
+    """A 1-D operand: contiguous, of exactly numel elements, on CUDA device `dev`."""
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{dev}" if dev >= 0 else ""))
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 1 or t.shape[0] != numel or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {numel} elements")
@@ -457,21 +468,21 @@ def fp8q_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, inte
               inverse: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotate bf16 heads x [T, H, D] by positions [T] (int64) times freq (fp64 [rot_dim / 2], from
     fp8q_rope_frequencies); elements from rot_dim on are copied.  `out` may be x itself."""
-    _require_heads(x, "x")
-    T, H, D = x.shape
-    _require_list(positions, "positions", torch.int64, T, x)
-    _require_list(freq, "freq", torch.float64, freq.shape[0] if freq.dim() else 0, x)
+    dev = x.get_device()
+    _require_heads(x, "x", dev)
+    shape = x.shape
+    T, H, D = shape
+    _require_list(positions, "positions", torch.int64, T, dev)
+    pairs = freq.numel()
+    _require_list(freq, "freq", torch.float64, pairs, dev)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
     elif out is not x:
-        _require_heads(out, "out", x, (T, H, D))
-    xt, xh = _head_strides(x)
-    yt, yh = _head_strides(out)
-    with _on(x):
-        st = lib().fp8q_rope(x.data_ptr(), T, H, D, xt, xh, positions.data_ptr(), freq.data_ptr(), 2 * freq.shape[0],
-                             (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0),
-                             float(mscale), out.data_ptr(), yt, yh, _stream(x))
-    _check(st, "fp8q_rope")
+        _require_heads(out, "out", dev, shape)
+    xt, xh = _head_strides(x, T, H, D)
+    yt, yh = _head_strides(out, T, H, D)
+    _call(dev, "fp8q_rope", x.data_ptr(), T, H, D, xt, xh, positions.data_ptr(), freq.data_ptr(), 2 * pairs,
+          (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), mscale, out.data_ptr(), yt, yh)
     return out
 
 
@@ -490,7 +501,7 @@ class KV4Cache:
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_size: int, head_dim: int = 128,
                  k_scale: float = 1.0, v_scale: float = 1.0):
         for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-            if not t.is_cuda or t.device != k_pages.device or t.dtype != torch.uint8:
+            if t.get_device() < 0 or t.get_device() != k_pages.get_device() or t.dtype != torch.uint8:
                 raise ValueError(f"{name} must be a uint8 CUDA tensor (both on one device)")
             if t.dim() != 3 or not t.is_contiguous() or t.shape != k_pages.shape or \
                     t.shape[2] != page_size * (head_dim * 9 // 16):
@@ -499,7 +510,7 @@ class KV4Cache:
         self.num_pages, self.kv_heads = int(k_pages.shape[0]), int(k_pages.shape[1])
         self.page_size, self.head_dim = int(page_size), int(head_dim)
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
-        self.device = k_pages.device
+        self.device, self._dev = k_pages.device, k_pages.get_device()
         self._struct = _CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), self.num_pages, self.page_size,
                                     self.kv_heads, self.head_dim, self.k_scale, self.v_scale)
         self._ref = ctypes.byref(self._struct)
@@ -518,50 +529,46 @@ def fp8q_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: to
                     interleaved: bool = False, mscale: float = 1.0) -> None:
     """Quantize k and v (bf16 [T, kv_heads, head_dim]) into the cache's slots ([T] int64, page * page_size + row;
     negative: skipped), k rotated by positions * freq on the way (as it is with both None)."""
-    _require_heads(k, "k", cache.k_pages)
+    dev = cache._dev
     T = k.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
-    _require_heads(k, "k", cache.k_pages, shape)
-    _require_heads(v, "v", cache.k_pages, shape)
-    _require_list(slots, "slots", torch.int64, T, k)
-    if (positions is None) != (freq is None):
+    _require_heads(k, "k", dev, shape)
+    _require_heads(v, "v", dev, shape)
+    _require_list(slots, "slots", torch.int64, T, dev)
+    R, pos, f = 0, None, None
+    if positions is not None and freq is not None:
+        _require_list(positions, "positions", torch.int64, T, dev)
+        R = 2 * freq.numel()
+        _require_list(freq, "freq", torch.float64, R // 2, dev)
+        pos, f = positions.data_ptr(), freq.data_ptr()
+    elif positions is not None or freq is not None:
         raise ValueError("positions and freq are given together")
-    R = 0
-    if positions is not None:
-        _require_list(positions, "positions", torch.int64, T, k)
-        _require_list(freq, "freq", torch.float64, freq.shape[0] if freq.dim() else 0, k)
-        R = 2 * freq.shape[0]
-    kt, kh = _head_strides(k)
-    vt, vh = _head_strides(v)
-    with _on(k):
-        st = lib().fp8q_kv4_append(cache._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), T,
-                                   _ptr(positions), _ptr(freq), R, ROPE_INTERLEAVED if interleaved else 0,
-                                   float(mscale), _stream(k))
-    _check(st, "fp8q_kv4_append")
+    kt, kh = _head_strides(k, *shape)
+    vt, vh = _head_strides(v, *shape)
+    _call(dev, "fp8q_kv4_append", cache._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), T, pos, f, R,
+          ROPE_INTERLEAVED if interleaved else 0, mscale)
 
 
 def fp8q_kv4_read(cache: KV4Cache, slots: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
     """The cached keys and values of slots [T] (int64) as bf16 [T, kv_heads, head_dim]; zeros for a negative slot."""
-    _require_list(slots, "slots", torch.int64, slots.shape[0] if slots.dim() else 0, cache.k_pages)
-    shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
+    dev, T = cache._dev, slots.numel()
+    _require_list(slots, "slots", torch.int64, T, dev)
+    shape = (T, cache.kv_heads, cache.head_dim)
     if out is None:
-        out = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device),
-               torch.empty(shape, dtype=torch.bfloat16, device=cache.device))
-    k, v = out
-    _require_heads(k, "k", cache.k_pages, shape)
-    _require_heads(v, "v", cache.k_pages, shape)
-    kt, kh = _head_strides(k)
-    vt, vh = _head_strides(v)
-    with _on(k):
-        st = lib().fp8q_kv4_read(cache._ref, slots.data_ptr(), shape[0], k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                 _stream(k))
-    _check(st, "fp8q_kv4_read")
+        k, v = torch.empty((2, *shape), dtype=torch.bfloat16, device=cache.device)
+    else:
+        k, v = out
+        _require_heads(k, "k", dev, shape)
+        _require_heads(v, "v", dev, shape)
+    kt, kh = _head_strides(k, *shape)
+    vt, vh = _head_strides(v, *shape)
+    _call(dev, "fp8q_kv4_read", cache._ref, slots.data_ptr(), T, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh)
     return k, v
 
 
 def fp8q_kv4_attention_workspace_size(cache: KV4Cache, num_seqs: int, tokens: int, q_heads: int,
                                       max_q_len: int = 1) -> int:
-    with _on(cache.k_pages):
+    with torch.cuda.device(cache._dev):
         return int(lib().fp8q_kv4_attention_workspace_size(cache._ref, num_seqs, tokens, q_heads, max_q_len))
 
 
@@ -576,43 +583,38 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tenso
     (None: one row per sequence).  Rows behind q_start[B] are left as they were.  lse: fp32 [T, q_heads], written
     when given.  `workspace`: a zero-filled uint8 buffer of fp8q_kv4_attention_workspace_size bytes (allocated here
     when None; left zero).  -> out bf16 [T, q_heads, head_dim]"""
-    ref = cache.k_pages
-    _require_heads(q, "q", ref)
-    T, Hq, D = q.shape
+    dev = cache._dev
+    _require_heads(q, "q", dev)
+    shape = q.shape
+    T, Hq, D = shape
     if D != cache.head_dim:
         raise ValueError(f"q must have head_dim {cache.head_dim}")
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != ref.device or \
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.get_device() != dev or \
+            (page_table.stride(1) != 1 and page_table.shape[1] > 1):
         raise ValueError("page_table must be int32 [sequences, max_pages] on the cache's device, rows contiguous")
     B, max_pages = page_table.shape
-    _require_list(kv_len, "kv_len", torch.int32, B, ref)
+    _require_list(kv_len, "kv_len", torch.int32, B, dev)
     if q_start is not None:
-        _require_list(q_start, "q_start", torch.int32, B + 1, ref)
+        _require_list(q_start, "q_start", torch.int32, B + 1, dev)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     else:
-        _require_heads(out, "out", ref, (T, Hq, D))
-    if lse is not None:
-        _require_out(lse, "lse", torch.float32, (T, Hq), ref)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
-    L = lib()
-    with _on(ref):
-        if workspace is None:
-            need = int(L.fp8q_kv4_attention_workspace_size(cache._ref, B, T, Hq, int(max_q_len)))
-            if need > 0:
-                workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-        else:                    # its size is checked by the library (FP8Q_ERR_INVALID_ARG)
-            _require_like(workspace, "workspace", torch.uint8, 0, ref)
-        qt, qh = _head_strides(q)
-        ot, oh = _head_strides(out)
-        st = L.fp8q_kv4_attention(cache._ref, q.data_ptr(), qt, qh, T, Hq, page_table.data_ptr(),
-                                  page_table.stride(0) if B > 1 else max_pages, max_pages, kv_len.data_ptr(),
-                                  _ptr(q_start), B, int(max_q_len),
-                                  float(D ** -0.5 if sm_scale is None else sm_scale), 1 if causal else 0, int(window),
-                                  out.data_ptr(), ot, oh, _ptr(lse), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel(), _stream(q))
-    _check(st, "fp8q_kv4_attention")
+        _require_heads(out, "out", dev, shape)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or
+                            not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous fp32 {(T, Hq)} on the cache's device")
+    if workspace is None:
+        workspace = torch.zeros(fp8q_kv4_attention_workspace_size(cache, B, T, Hq, max_q_len), dtype=torch.uint8,
+                                device=q.device)
+    elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+    qt, qh = _head_strides(q, T, Hq, D)
+    ot, oh = _head_strides(out, T, Hq, D)
+    _call(dev, "fp8q_kv4_attention", cache._ref, q.data_ptr(), qt, qh, T, Hq, page_table.data_ptr(),
+          page_table.stride(0) if B > 1 else max_pages, max_pages, kv_len.data_ptr(),
+          None if q_start is None else q_start.data_ptr(), B, max_q_len, D ** -0.5 if sm_scale is None else sm_scale,
+          1 if causal else 0, window, out.data_ptr(), ot, oh, None if lse is None else lse.data_ptr(),
+          workspace.data_ptr(), workspace.numel())     # its size is checked by the library (FP8Q_ERR_INVALID_ARG)
     return out
 
 

@@ -209,8 +209,23 @@ fp8q_status fp8q_rope(const void* X_bf16, int64_t T, int64_t H, int64_t D, int64
   p.m = mscale;
   p.interleaved = (flags & FP8Q_ROPE_INTERLEAVED) != 0;
   p.inverse = (flags & FP8Q_ROPE_INVERSE) != 0;
-  return launch(fp8q::rope::rope_kernel, dim3(blocks_for(T * H * (rot_dim / 2), 256, 8ll * sms)), dim3(256), 0, stream,
-                p);
+  // 16-byte rows take the vector kernel; anything else, one pair a thread
+  const bool vec = rot_dim % 16 == 0 && D % 8 == 0 && rot_dim <= 1024 && aligned(X_bf16, 16) && aligned(Y_bf16, 16) &&
+                   (T == 1 || (x_token_stride % 8 == 0 && y_token_stride % 8 == 0)) &&
+                   (H == 1 || (x_head_stride % 8 == 0 && y_head_stride % 8 == 0));
+  if (!vec)
+    return launch(fp8q::rope::rope_any_kernel, dim3(blocks_for(T * H * (rot_dim / 2), 256, 8ll * sms)), dim3(256), 0,
+                  stream, p);
+  // Four tokens a CTA share the launch and the angles where that still gives every SM several CTAs; a few tokens are
+  // spread over the SMs by heads instead.
+  const int tokens = T >= 16ll * sms ? 4 : 1;
+  const int64_t units = H * (rot_dim / 16);
+  int64_t split = T < sms ? (units + 511) / 512 : 1;
+  if (split > H) split = H;
+  const dim3 grid(static_cast<unsigned>((T + tokens - 1) / tokens), static_cast<unsigned>(split));
+  const size_t bytes = static_cast<size_t>(tokens) * (rot_dim / 2) * sizeof(float2);
+  auto k = p.interleaved ? fp8q::rope::rope_vec_kernel<true> : fp8q::rope::rope_vec_kernel<false>;
+  return launch(k, grid, dim3(256), bytes, stream, p, tokens);
 }
 
 size_t fp8q_kv4_page_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim) {
@@ -255,7 +270,9 @@ fp8q_status fp8q_kv4_append(const fp8q_kv4_cache* cache, const void* K_bf16, int
   p.interleaved = (flags & FP8Q_ROPE_INTERLEAVED) != 0;
   p.m = mscale;
   auto k = cache->head_dim == 64 ? fp8q::kv4::append_kernel<64> : fp8q::kv4::append_kernel<128>;
-  return launch(k, dim3(blocks_for(2 * T * cache->kv_heads, 8, kInt32Max)), dim3(256), 0, stream, p);
+  const int tokens = T >= 16ll * sms ? 4 : 1;      // as in fp8q_rope
+  return launch(k, dim3(blocks_for(T, tokens, kInt32Max)), dim3(256),
+                static_cast<size_t>(tokens) * (p.R / 2) * sizeof(double2), stream, p, tokens);
 }
 
 fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* slots, int64_t T, void* K_bf16,
@@ -285,8 +302,9 @@ fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* slots, int
   p.vt = v_token_stride;
   p.vh = v_head_stride;
   p.T = static_cast<int>(T);
-  const int64_t items = 2 * T * cache->kv_heads * (cache->head_dim / 16);
-  return launch(fp8q::kv4::read_kernel, dim3(blocks_for(items, 256, 8ll * sms)), dim3(256), 0, stream, p);
+  const int64_t items = 2 * T * cache->kv_heads * (cache->head_dim / 8);
+  auto k = cache->head_dim == 64 ? fp8q::kv4::read_kernel<64> : fp8q::kv4::read_kernel<128>;
+  return launch(k, dim3(blocks_for(items, 512, 8ll * sms)), dim3(256), 0, stream, p);
 }
 
 size_t fp8q_kv4_attention_workspace_size(const fp8q_kv4_cache* cache, int64_t B, int64_t T, int64_t Hq,

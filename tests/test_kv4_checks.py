@@ -230,15 +230,15 @@ def test_attention_arguments(L, kw, want):
 class S(T):
     """The stand-in with what the cache's binding reads besides."""
 
-    def element_size(self):
-        return {U8: 1, BF: 2, F32: 4, I32: 4, I64: 8, F64: 8}[self.dtype]
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
 
 
 @pytest.fixture
 def lib(monkeypatch):
     rec = Lib()
     monkeypatch.setattr(fq, "lib", lambda: rec)
-    monkeypatch.setattr(fq, "_stream", lambda t: 0)
+    monkeypatch.setattr(fq, "_raw_stream", lambda dev: 0)
     monkeypatch.setattr(fq.torch.cuda, "current_device", lambda: 0)
     return rec
 
@@ -305,7 +305,7 @@ def test_binding_attention(lib):
                 workspace=S((64,), U8))
     call = lambda **kw: fq.fp8q_kv4_attention(**{**base, **kw})  # noqa: E731
     call()
-    call(q_start=None, lse=None, workspace=None)       # the recorder's workspace size is 0
+    call(q_start=None, lse=None)
     assert lib.calls.count("fp8q_kv4_attention") == 2
     refused(lib, "fp8q_kv4_attention", call,
             q=[S((7, 8, 64), BF), S((7, 8, 128), F32), S((7, 1024), BF), S((7, 8, 128), BF, device=CUDA1)],
