@@ -272,7 +272,7 @@ fp8q_status fp8q_kv4_append(const fp8q_kv4_cache* cache, const void* K_bf16, int
   auto k = cache->head_dim == 64 ? fp8q::kv4::append_kernel<64> : fp8q::kv4::append_kernel<128>;
   const int tokens = T >= 16ll * sms ? 4 : 1;      // as in fp8q_rope
   return launch(k, dim3(blocks_for(T, tokens, kInt32Max)), dim3(256),
-                static_cast<size_t>(tokens) * (p.R / 2) * sizeof(double2), stream, p, tokens);
+                static_cast<size_t>(tokens) * (cache->head_dim / 2) * sizeof(double2), stream, p, tokens);
 }
 
 fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* slots, int64_t T, void* K_bf16,
@@ -302,9 +302,9 @@ fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* slots, int
   p.vt = v_token_stride;
   p.vh = v_head_stride;
   p.T = static_cast<int>(T);
-  const int64_t items = 2 * T * cache->kv_heads * (cache->head_dim / 8);
+  const int64_t items = 2 * T * cache->kv_heads * (cache->head_dim / 16);
   auto k = cache->head_dim == 64 ? fp8q::kv4::read_kernel<64> : fp8q::kv4::read_kernel<128>;
-  return launch(k, dim3(blocks_for(items, 512, 8ll * sms)), dim3(256), 0, stream, p);
+  return launch(k, dim3(blocks_for(items, 512, kInt32Max)), dim3(256), 0, stream, p);
 }
 
 size_t fp8q_kv4_attention_workspace_size(const fp8q_kv4_cache* cache, int64_t B, int64_t T, int64_t Hq,

@@ -89,127 +89,144 @@ struct AppendParams {
   float m;
 };
 
-// x / s, correctly rounded, for the values of a block with amax |x| (the
-// correction step of quant.cuh's Divider; its range, narrowed so that nothing
-// overflows here).  Quotients too small for the residual to be exact are far
-// below the smallest code; the sign is x's.
-struct BlockDivider {
-  float s, y;
-  bool fast;
-};
-__device__ __forceinline__ float divide(float x, const BlockDivider& d) {
-  if (!d.fast) return __fdiv_rn(x, d.s);
-  const float q = x * d.y;
-  return copysignf(fmaf(fmaf(-q, d.s, x), d.y, q), x);
+// Two quotients x / s, correctly rounded, from the negated values (the
+// correction step of quant.cuh's Divider, on packed fp32; it runs on -x so that
+// a zero keeps its sign).  y = RN(1 / s).  Right where s lies in [2^-60, 2^60]
+// and |x| <= 2^60: nothing overflows, and quotients too small for the residual
+// to be exact are far below the smallest code.
+__device__ __forceinline__ uint32_t encode2(float nx0, float nx1, uint64_t ny2, uint64_t s2) {
+  const uint64_t nx = f32x2_pack(nx0, nx1), q = mul_f32x2(nx, ny2), r = fma_f32x2(q, s2, nx);
+  float q0, q1;
+  f32x2_unpack(fma_f32x2(r, ny2, q), q0, q1);
+  return cvt_e2m1x2(q0, q1);
 }
 
-// Bound by HBM for prompts (2 bytes read an element, 9/16 written), by its
-// latency for single tokens.  A CTA takes `tokens` tokens: its threads compute
-// the tokens' angles into shared memory, once for all heads (an fp64 sincos
-// each), with the first rows' loads on the way.  A warp then takes rows of one
-// token's K or V, kBatch at a time; a lane holds four elements of a row (a
-// half warp a row at D = 64).  K is rotated in fp64 and rounded once to fp32:
-// with fp32 products a value next to a code's border could get another code
-// than its definition gives, a whole E2M1 step away.
-constexpr int kBatch = 4;
-
+// Bound by HBM for prompts (2 bytes read an element, 9/16 written) as far as
+// the instructions allow, by its latency for single tokens.  A CTA takes
+// `tokens` tokens: its threads compute the tokens' angles into shared memory,
+// once for all heads (an fp64 sincos each), with the first blocks' loads on the
+// way.  A thread keeps its place (head, block of 16 elements) and walks over
+// the tokens' K and V: the scale is computed once for 16 values and nothing is
+// exchanged between lanes.  K is rotated in fp64 and rounded once to fp32: with
+// fp32 products a value next to a code's border could get another code than
+// its definition gives, a whole E2M1 step away.  A block's partners (half
+// layout) are read from memory as well; they are another thread's elements, so
+// they come from L1.
 template <int D>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p, int tokens) {
-  constexpr int kLanes = D / 4, kRowsPerWarp = 32 / kLanes, kGroup = kBatch * kRowsPerWarp;
-  extern __shared__ double2 angles[];               // [tokens][R / 2] (cos, sin)
+__global__ void __launch_bounds__(256, 4) append_kernel(const __grid_constant__ AppendParams p, int tokens) {
+  constexpr int kBlocks = D / 16, kCols = D / 32;
+  // [tokens][16][kCols] (cos, sin); pair f at (f % 16, f / 16): for one element of their blocks, neighbouring threads
+  // read neighbouring entries
+  extern __shared__ double2 angles[];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = lane_id(), warp = threadIdx.x >> 5;
-  const int l = lane % kLanes, sub = lane / kLanes;
   const int t0 = blockIdx.x * tokens, nt = min(tokens, p.T - t0);
-  const int groups = (p.c.heads + kGroup - 1) / kGroup, half = p.R / 2;
-  const int list = nt * 2 * groups;                 // (token, K or V, group of heads)
-  // this lane's place in a rotated row: its angles' index, and (half layout) the lane that holds its partners
-  const int d = 4 * l;
-  const bool turned = d < p.R, second = !p.interleaved && d >= half;
-  const int f = p.interleaved ? d / 2 : (second ? d - half : d);
-  const int partner = turned && !p.interleaved ? lane + (second ? -half / 4 : half / 4) : lane;
+  const int half = p.R / 2, places = p.c.heads * kBlocks;
+  const int groups = max(1, 256 / places), group = threadIdx.x / places;
+  const float kg6 = __fmul_rn(6.0f, p.c.kg), vg6 = __fmul_rn(6.0f, p.c.vg);
   bool first = true;
-  for (int i = warp; i < list || first; i += 8) {
-    const int t = i / (2 * groups), rest = i - t * 2 * groups, is_v = rest >= groups, h0 = (is_v ? rest - groups : rest) * kGroup;
-    uint2 raw[kBatch];
-    int64_t slot = -1;
-    if (i < list) {
-      slot = p.slots[t0 + t];
-      const uint16_t* x = is_v ? p.v + (t0 + t) * p.vt : p.k + (t0 + t) * p.kt;
-      const int64_t xh = is_v ? p.vh : p.kh;
+  for (int place = threadIdx.x - group * places; place < places || first; place += 256) {
+    const int h = place / kBlocks, d0 = place % kBlocks * 16;
+    const bool turns = p.pos != nullptr && d0 < p.R;
+    for (int j = group; j < 2 * nt || first; j += groups) {
+      const bool there = j < 2 * nt && group < groups && place < places;
+      const int t = j >> 1;
+      const bool is_v = j & 1;
+      const bool turn = turns && !is_v;
+      uint32_t raw[8];
+      uint2 other[4];
+      int64_t slot = -1;
+      if (there) {
+        slot = p.slots[t0 + t];
+        const uint16_t* x = is_v ? p.v + (t0 + t) * p.vt + h * p.vh : p.k + (t0 + t) * p.kt + h * p.kh;
+        const uint4 lo = *reinterpret_cast<const uint4*>(x + d0), hi = *reinterpret_cast<const uint4*>(x + d0 + 8);
+        raw[0] = lo.x; raw[1] = lo.y; raw[2] = lo.z; raw[3] = lo.w;
+        raw[4] = hi.x; raw[5] = hi.y; raw[6] = hi.z; raw[7] = hi.w;
+        if (turn && !p.interleaved) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int h = h0 + b * kRowsPerWarp + sub;
-        raw[b] = make_uint2(0, 0);
-        if (h < p.c.heads) raw[b] = *reinterpret_cast<const uint2*>(x + h * xh + d);
-      }
-    }
-    if (first) {
-      first = false;
-      if (p.pos != nullptr) {
-        for (int j = threadIdx.x; j < nt * half; j += 256) {
-          double s, c;
-          sincospi(rope::half_turns(p.pos[t0 + j / half], p.freq[j % half]), &s, &c);
-          angles[j] = make_double2(c * p.m, s * p.m);
+          for (int q = 0; q < 4; ++q) {              // R is a multiple of 8: four elements change sides together
+            const int d = d0 + 4 * q;
+            if (d < p.R) other[q] = *reinterpret_cast<const uint2*>(x + (d < half ? d + half : d - half));
+          }
         }
-        __syncthreads();
       }
-      if (i >= list) return;
-    }
-    if (slot < 0) continue;
-    if (slot >= p.c.pages * p.c.page_size) {
-      if (lane == 0) atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadSlot));
-      continue;
-    }
-    const float g = is_v ? p.c.vg : p.c.kg, g6 = __fmul_rn(6.0f, g);
-    uint8_t* base = is_v ? p.c.v : p.c.k;
-    const int64_t page = slot >> p.c.page_shift;
-    const int row = static_cast<int>(slot) & (p.c.page_size - 1);
-    double2 cs[4];
-    const bool turn = p.pos != nullptr && !is_v;
-    if (turn && turned) {
+      if (first) {
+        first = false;
+        if (p.pos != nullptr) {
+          for (int i = threadIdx.x; i < nt * half; i += 256) {
+            const int u = i / half, f = i - u * half;
+            angles[(u * 16 + (f & 15)) * kCols + (f >> 4)] = rope::cos_sin_f64(p.pos[t0 + u], p.freq[f], p.m);
+          }
+          __syncthreads();
+        }
+        if (!there) return;
+      }
+      if (slot < 0) continue;
+      if (slot >= p.c.pages * p.c.page_size) {
+        atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadSlot));
+        continue;
+      }
+      float a[16];                                   // the negated values
 #pragma unroll
-      for (int e = 0; e < 4; ++e) cs[e] = angles[t * half + (p.interleaved ? f + e / 2 : f + e)];
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int h = h0 + b * kRowsPerWarp + sub;
-      float a[4] = {bf16lo(raw[b].x), bf16hi(raw[b].x), bf16lo(raw[b].y), bf16hi(raw[b].y)};
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t n = raw[e] ^ 0x80008000u;
+        a[2 * e] = bf16lo(n);
+        a[2 * e + 1] = bf16hi(n);
+      }
       if (turn) {
-        uint2 other = raw[b];
-        if (!p.interleaved) {
-          other.x = __shfl_sync(0xFFFFFFFFu, raw[b].x, partner);
-          other.y = __shfl_sync(0xFFFFFFFFu, raw[b].y, partner);
-        }
-        if (turned) {
-          float o[4] = {bf16lo(other.x), bf16hi(other.x), bf16lo(other.y), bf16hi(other.y)};
-          if (p.interleaved) {
-            const float y0 = o[0], y2 = o[2];
-            o[0] = o[1]; o[1] = y0; o[2] = o[3]; o[3] = y2;
-          }
+        const double2* table = angles + t * 16 * kCols;
+        if (p.interleaved) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool back = p.interleaved ? (e & 1) : second;          // the pair's second element
-            const double mine = a[e], its = o[e];
-            a[e] = __double2float_rn(fma(mine, cs[e].x, back ? its * cs[e].y : -its * cs[e].y));
+          for (int e = 0; e < 16; e += 2) {
+            if (d0 + e < p.R) {
+              const int f = (d0 + e) / 2;
+              const double2 cs = table[(f & 15) * kCols + (f >> 4)];
+              const double x0 = a[e], x1 = a[e + 1];
+              a[e] = __double2float_rn(fma(x0, cs.x, -x1 * cs.y));
+              a[e + 1] = __double2float_rn(fma(x1, cs.x, x0 * cs.y));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int d = d0 + 4 * q;
+            if (d < p.R) {
+              const bool second = d >= half;
+              const int f = second ? d - half : d;   // a multiple of 4: its four pairs lie kCols apart
+              const double2* cs = table + (f & 15) * kCols + (f >> 4);
+              const uint32_t sign = second ? 0x80008000u : 0u;             // -its x1's sign in y0, +its x0's in y1, negated
+              const uint32_t o0 = other[q].x ^ sign, o1 = other[q].y ^ sign;
+              const float o[4] = {bf16lo(o0), bf16hi(o0), bf16lo(o1), bf16hi(o1)};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const double2 c = cs[e * kCols];
+                a[4 * q + e] = __double2float_rn(fma(static_cast<double>(a[4 * q + e]), c.x, static_cast<double>(o[e]) * c.y));
+              }
+            }
           }
         }
       }
-      float amax = fmaxf(fmaxf(fabsf(a[0]), fabsf(a[1])), fmaxf(fabsf(a[2]), fabsf(a[3])));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      BlockDivider dv;
-      const uint32_t sc = scale_code(amax, g, g6, &dv.s);
-      dv.y = __frcp_rn(dv.s);
-      dv.fast = dv.s >= 0x1p-60f && dv.s <= 0x1p60f && amax <= 0x1p60f;
-      uint32_t codes = 0;
-      if (dv.s > 0.0f)
-        codes = cvt_e2m1x2(divide(a[0], dv), divide(a[1], dv)) | (cvt_e2m1x2(divide(a[2], dv), divide(a[3], dv)) << 8);
-      if (h < p.c.heads) {
-        *reinterpret_cast<uint16_t*>(base + p.c.code_offset(page, h, row) + d / 2) = static_cast<uint16_t>(codes);
-        if ((l & 3) == 0) base[p.c.scale_offset(page, h, row) + l / 4] = static_cast<uint8_t>(sc);
+      float amax = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) amax = fmaxf(fmaxf(fabsf(a[e]), fabsf(a[e + 1])), amax);
+      float s;
+      const uint32_t sc = scale_code(amax, is_v ? p.c.vg : p.c.kg, is_v ? vg6 : kg6, &s);
+      uint32_t codes[2] = {0, 0};
+      if (s >= 0x1p-60f && s <= 0x1p60f && amax <= 0x1p60f) {
+        const float y = -__frcp_rn(s);
+        const uint64_t ny2 = f32x2_pack(y, y), s2 = f32x2_pack(s, s);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) codes[e / 8] |= encode2(a[e], a[e + 1], ny2, s2) << (4 * (e % 8));
+      } else if (s > 0.0f) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          codes[e / 8] |= cvt_e2m1x2(__fdiv_rn(-a[e], s), __fdiv_rn(-a[e + 1], s)) << (4 * (e % 8));
       }
+      uint8_t* base = is_v ? p.c.v : p.c.k;
+      const int64_t page = slot >> p.c.page_shift;
+      const int row = static_cast<int>(slot) & (p.c.page_size - 1);
+      *reinterpret_cast<uint2*>(base + p.c.code_offset(page, h, row) + d0 / 2) = make_uint2(codes[0], codes[1]);
+      base[p.c.scale_offset(page, h, row) + d0 / 16] = static_cast<uint8_t>(sc);
     }
   }
 }
@@ -224,18 +241,19 @@ struct ReadParams {
 };
 
 // The cached values of the given slots as bf16 (zeros for a negative slot): one
-// thread per 8 elements (a 16-byte store), two in flight.
+// thread per 16 elements, two in flight.
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int kParts = D / 8, kFlight = 2;
+  constexpr int kBlocks = D / 16, kFlight = 2;
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t heads = static_cast<uint32_t>(p.c.heads), per_token = 2 * heads;
   const uint32_t rows = static_cast<uint32_t>(p.T) * per_token;          // (token, K or V, head)
-  const int part = threadIdx.x % kParts;
-  const uint32_t step = gridDim.x * (256 / kParts);
-  for (uint32_t r = blockIdx.x * (256 / kParts) + threadIdx.x / kParts; r < rows; r += kFlight * step) {
-    uint32_t codes[kFlight], scale[kFlight];
+  const int block = threadIdx.x % kBlocks;
+  const uint32_t step = gridDim.x * (256 / kBlocks);
+  for (uint32_t r = blockIdx.x * (256 / kBlocks) + threadIdx.x / kBlocks; r < rows; r += kFlight * step) {
+    uint2 codes[kFlight];
+    uint32_t scale[kFlight];
     uint16_t* y[kFlight];
     float g[kFlight];
 #pragma unroll
@@ -251,28 +269,30 @@ __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadP
         atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadSlot));
         slot = -1;
       }
-      y[i] = (is_v ? p.v + t * p.vt + h * p.vh : p.k + t * p.kt + h * p.kh) + part * 8;
+      y[i] = (is_v ? p.v + t * p.vt + h * p.vh : p.k + t * p.kt + h * p.kh) + block * 16;
       g[i] = is_v ? p.c.vg : p.c.kg;
-      codes[i] = scale[i] = 0;
+      codes[i] = make_uint2(0, 0);
+      scale[i] = 0;
       if (slot >= 0) {
         const uint8_t* base = is_v ? p.c.v : p.c.k;
         const int64_t page = slot >> p.c.page_shift;
         const int in_page = static_cast<int>(slot) & (p.c.page_size - 1);
-        codes[i] = *reinterpret_cast<const uint32_t*>(base + p.c.code_offset(page, h, in_page) + part * 4);
-        scale[i] = base[p.c.scale_offset(page, h, in_page) + part / 2];
+        codes[i] = *reinterpret_cast<const uint2*>(base + p.c.code_offset(page, h, in_page) + block * 8);
+        scale[i] = base[p.c.scale_offset(page, h, in_page) + block];
       }
     }
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
       if (y[i] == nullptr) continue;
       const float s = f16lo(widen_e4m3x2(scale[i]));
-      uint32_t o[4];
+      uint32_t o[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {                  // code * scale is exact; then one fp32 product, one rounding to bf16
-        const uint32_t w = widen_e2m1x2(codes[i] >> (8 * j));
+      for (int j = 0; j < 8; ++j) {                  // code * scale is exact; then one fp32 product, one rounding to bf16
+        const uint32_t w = widen_e2m1x2((j < 4 ? codes[i].x : codes[i].y) >> (8 * (j & 3)));
         o[j] = pack_bf16x2(f16lo(w) * s * g[i], f16hi(w) * s * g[i]);
       }
-      *reinterpret_cast<uint4*>(y[i]) = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4*>(y[i])[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4*>(y[i])[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
 }

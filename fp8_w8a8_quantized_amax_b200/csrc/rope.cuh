@@ -18,15 +18,44 @@ namespace rope {
 // positions (at p = 131072 and f = 1, a step of fp32 is 0.008 radians).
 constexpr double kTurnsPerRadian = 0.15915494309189533577;
 
-__device__ __forceinline__ double half_turns(int64_t p, double f) {
+// The fraction of a turn, in [-1/2, 1/2].
+__device__ __forceinline__ double turn(int64_t p, double f) {
   const double t = static_cast<double>(p) * (f * kTurnsPerRadian);
-  return 2.0 * (t - rint(t));
+  return t - rint(t);
 }
 
 __device__ __forceinline__ float2 cos_sin(int64_t p, double f, float m, bool inverse) {
   float s, c;
-  sincospif(static_cast<float>(half_turns(p, f)), &s, &c);   // |half turns| <= 1: fp32 is off by 2^-25 of a turn
+  sincospif(static_cast<float>(2.0 * turn(p, f)), &s, &c);   // |half turns| <= 1: fp32 is off by 2^-25 of a turn
   return make_float2(c * m, inverse ? -s * m : s * m);
+}
+
+// The same in fp64, by the Taylor series on an eighth of a turn to either side
+// of the nearest quarter: with |x| <= pi / 4 the first terms left out are
+// x^17 / 17! < 5e-17 and x^18 / 18! < 3e-18.  (The library's sincospi took a
+// third of the append kernel's instructions.)
+__device__ __forceinline__ double2 cos_sin_f64(int64_t p, double f, double m) {
+  const double r = turn(p, f), quarter = rint(4.0 * r);
+  const double x = 6.283185307179586477 * fma(quarter, -0.25, r), z = x * x;
+  double s = -1.0 / 1307674368000.0, c = 1.0 / 20922789888000.0;
+  s = fma(s, z, 1.0 / 6227020800.0);
+  c = fma(c, z, -1.0 / 87178291200.0);
+  s = fma(s, z, -1.0 / 39916800.0);
+  c = fma(c, z, 1.0 / 479001600.0);
+  s = fma(s, z, 1.0 / 362880.0);
+  c = fma(c, z, -1.0 / 3628800.0);
+  s = fma(s, z, -1.0 / 5040.0);
+  c = fma(c, z, 1.0 / 40320.0);
+  s = fma(s, z, 1.0 / 120.0);
+  c = fma(c, z, -1.0 / 720.0);
+  s = fma(s, z, -1.0 / 6.0);
+  c = fma(c, z, 1.0 / 24.0);
+  s = fma(s * z, x, x);
+  c = fma(c, z, -0.5);
+  c = fma(c, z, 1.0);
+  const int q = static_cast<int>(quarter) & 3;     // cos and sin of q quarters and x
+  const double a = (q & 1) ? s : c, b = (q & 1) ? c : s;
+  return make_double2((q == 1 || q == 2) ? -a * m : a * m, (q & 2) ? -b * m : b * m);
 }
 
 struct Params {
@@ -72,11 +101,11 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ P
 // bytes), with their first loads already on the way.  A unit is eight pairs:
 // two 16-byte vectors, R / 2 apart (half layout) or side by side (interleaved).
 // A thread walks the units u, u + 256, ... of the CTA's (token, head, unit)
-// list, four in flight.
-constexpr int kUnits = 4;
+// list, two in flight.
+constexpr int kUnits = 2;
 
 template <bool INTERLEAVED>
-__global__ void __launch_bounds__(256) rope_vec_kernel(const __grid_constant__ Params p, int tokens) {
+__global__ void __launch_bounds__(256, 4) rope_vec_kernel(const __grid_constant__ Params p, int tokens) {
   extern __shared__ float2 table[];                 // [tokens][R / 2]
   griddep_wait();
   griddep_launch_dependents();
