@@ -89,8 +89,8 @@ AttentionPlan attention_plan(const fp8q_kv4_cache* c, int64_t T, int64_t Hq, int
   const int64_t rows = (max_q_len < T ? max_q_len : T) * (Hq / c->kv_heads);
   AttentionPlan a;
   a.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 32 ? 4 : 0));
-  a.ctas = sms * (a.nt == 1 ? 4 : (a.nt == 2 ? 3 : (a.nt == 4 ? 2 : 1)));
-  const int most = static_cast<int>(kWorkspaceHeader / (2 * sizeof(unsigned)));   // two counters a CTA at most
+  a.ctas = sms * (a.nt == 1 ? 5 : (a.nt == 2 ? 3 : (a.nt == 4 ? 2 : 1)));
+  const int most = static_cast<int>(kWorkspaceHeader / sizeof(unsigned)) / (a.nt ? 1 : 2);   // counters a CTA: 1 or 2
   if (a.ctas > most) a.ctas = most;
   const int64_t tile = a.nt ? 8 * a.nt : fp8q::kv4::many::kRows;
   a.row_tiles = static_cast<int>((rows + tile - 1) / tile);
@@ -370,12 +370,12 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
   p.row_tiles = plan.row_tiles;
   if (cache->head_dim == 128) {
-    if (plan.nt == 1) return launch_few<128, 1, 4>(p, plan.ctas, dev, stream);
+    if (plan.nt == 1) return launch_few<128, 1, 5>(p, plan.ctas, dev, stream);
     if (plan.nt == 2) return launch_few<128, 2, 3>(p, plan.ctas, dev, stream);
     if (plan.nt == 4) return launch_few<128, 4, 2>(p, plan.ctas, dev, stream);
     return launch_many<128>(p, plan.ctas, dev, stream);
   }
-  if (plan.nt == 1) return launch_few<64, 1, 4>(p, plan.ctas, dev, stream);
+  if (plan.nt == 1) return launch_few<64, 1, 5>(p, plan.ctas, dev, stream);
   if (plan.nt == 2) return launch_few<64, 2, 3>(p, plan.ctas, dev, stream);
   if (plan.nt == 4) return launch_few<64, 4, 2>(p, plan.ctas, dev, stream);
   return launch_many<64>(p, plan.ctas, dev, stream);

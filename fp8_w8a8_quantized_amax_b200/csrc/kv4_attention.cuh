@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -112,7 +112,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // The first product of a sum: no accumulator to read.
 __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %10, %10, %10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -161,6 +161,10 @@ namespace few {
 constexpr int kTile = 32;     // keys of a warp per step
 constexpr int kStages = 2;
 
+// Q fragments in shared memory instead of 16 NT registers: at 32 rows and at 8 (where five CTAs then fit an SM).
+template <int NT>
+constexpr bool kQInSmem = NT != 2;
+
 template <int D, int NT, int WARPS>
 struct Layout {
   static constexpr int kThreads = 32 * WARPS;
@@ -169,10 +173,13 @@ struct Layout {
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);       // K codes, K scales, V codes, V scales
   static constexpr int kRedStride = D + 4;
-  static constexpr int kRed = WARPS * kStages * kStageBytes;       // [WARPS][kRows][kRedStride] fp32
-  static constexpr int kMl = kRed + WARPS * kRows * kRedStride * 4;   // [WARPS][kRows] m, then l
-  static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // NT = 4: Q fragments
-  static constexpr int kMisc = kQ + (NT == 4 ? NT * (D / 16) * 32 * 8 : 0);
+  // [kRows][kRedStride] fp32 a warp: over the warp's free stage where it fits (it does at NT = 1), else apart
+  static constexpr bool kRedInStage = kRows * kRedStride * 4 <= kStageBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kRed = WARPS * kWarpBytes;
+  static constexpr int kMl = kRed + (kRedInStage ? 0 : WARPS * kRows * kRedStride * 4);   // [WARPS][kRows] m, then l
+  static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // Q fragments, where they are kept in shared memory
+  static constexpr int kMisc = kQ + (kQInSmem<NT> ? NT * (D / 16) * 32 * 8 : 0);
   static constexpr int kJobs = kMisc + 128;                        // two jobs of at most 64 bytes
   static constexpr int kBytes = kJobs + 128;
   static constexpr int kPart = kRows * (D + 2);                    // floats of a partial result
@@ -232,7 +239,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = lane_id(), warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  float* red = reinterpret_cast<float*>(smem + L::kRed);
+  // warp w's partial O^T at the end of a job; `stage` is then the stage of the next tile, in flight, and the other free
+  auto red_of = [&](int w, int stage) {
+    return reinterpret_cast<float*>(L::kRedInStage ? smem + w * L::kWarpBytes + (stage ^ 1) * L::kStageBytes
+                                                   : smem + L::kRed + w * kRows * L::kRedStride * 4);
+  };
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
   uint2* qs = reinterpret_cast<uint2*>(smem + L::kQ);
   Job* jobs = reinterpret_cast<Job*>(smem + L::kJobs);             // two: the current one and its successor
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
                       ((key + scale_key) & in_page) * (D / 16));
   };
 
-  uint32_t qf[NT == 4 ? 1 : NT][kSteps][2];
+  uint32_t qf[kQInSmem<NT> ? 1 : NT][kSteps][2];
   // per row: the scores' factor, the base m (negated; 0 before the first key), the score at which it is raised, the sum
   float qscale[NT][2], nbase[NT][2], limit[NT][2], l[NT][2];
   int pos[NT][2];
@@ -399,7 +410,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       for (int i = 0; i < kSteps; ++i) {
         const uint32_t b0 = pack_f16x2(bf16lo(w[2 * i]) * up, bf16hi(w[2 * i]) * up);
         const uint32_t b1 = pack_f16x2(bf16lo(w[2 * i + 1]) * up, bf16hi(w[2 * i + 1]) * up);
-        if constexpr (NT == 4) {
+        if constexpr (kQInSmem<NT>) {
           if (warp == nt % WARPS) qs[(nt * kSteps + i) * 32 + lane] = make_uint2(b0, b1);
         } else {
           qf[nt][i][0] = b0;
@@ -488,7 +499,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               uint32_t b0, b1;
-              if constexpr (NT == 4) {
+              if constexpr (kQInSmem<NT>) {
                 const uint2 v = qs[(nt * kSteps + 2 * w + h) * 32 + lane];
                 b0 = v.x;
                 b1 = v.y;
@@ -632,7 +643,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
         float top = -INFINITY;
         for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
         const float f = limit[nt][i] == -INFINITY ? 0.0f : ex2(-nbase[nt][i] - top);
-        float* dst = red + (warp * kRows + r) * L::kRedStride + g * (D / 8);
+        float* dst = red_of(warp, stage) + r * L::kRedStride + g * (D / 8);
 #pragma unroll
         for (int d = 0; d < kSteps; d += 2)
           *reinterpret_cast<float4*>(dst + 2 * d) = make_float4(o[d][nt][i] * f, o[d][nt][i + 2] * f,
@@ -662,7 +673,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       for (int w = 0; w < WARPS; ++w) {
         const float mw = ml[w * kRows + r];
         if (mw != -INFINITY) sum += ml[(WARPS + w) * kRows + r] * ex2(mw - top);
-        const float4 x = *reinterpret_cast<const float4*>(red + (w * kRows + r) * L::kRedStride + d);
+        const float4 x = *reinterpret_cast<const float4*>(red_of(w, stage) + r * L::kRedStride + d);
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
       if (!split) {
@@ -688,7 +699,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       if (static_cast<int>(misc[10]) == parts - 1) {
         __threadfence();
         // Per part a factor exp2(m_c - m), in shared memory (as many parts at a time as fit); then the sums.
-        constexpr int kMost = WARPS * L::kRedStride;                 // parts: kMost * kRows floats fit `red`
+        constexpr int kMost = L::kRedStride;                         // parts: kMost * kRows floats fit one warp's `red`
+        float* red = red_of(0, stage);
         float4 acc[kRows * (D / 4) / L::kThreads];
         float tops[kRows * (D / 4) / L::kThreads], sums[kRows * (D / 4) / L::kThreads];
 #pragma unroll
