@@ -75,8 +75,8 @@ fp8q_status check_rows(const void* p, int64_t t, int64_t h) {
 
 // What a call of these sizes launches: the kernel for few rows with 8 nt rows a
 // tile, or (nt = 0) the one for many; `ctas` CTAs; and the workspace: a header
-// of arrival counters, one per CTA, then two partial results per CTA.
-constexpr size_t kWorkspaceHeader = 4096;
+// of arrival counters, two per CTA, then two partial results per CTA.
+constexpr size_t kWorkspaceHeader = 2 * fp8q::kv4::kMaxCtas * sizeof(unsigned);
 static_assert(kWorkspaceHeader == FP8Q_KV4_WORKSPACE_HEADER, "as declared");
 
 struct AttentionPlan {
@@ -89,8 +89,8 @@ AttentionPlan attention_plan(const fp8q_kv4_cache* c, int64_t T, int64_t Hq, int
   const int64_t rows = (max_q_len < T ? max_q_len : T) * (Hq / c->kv_heads);
   AttentionPlan a;
   a.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 32 ? 4 : 0));
-  a.ctas = sms * (a.nt == 1 ? 5 : (a.nt == 2 ? 3 : (a.nt == 4 ? 2 : 1)));
-  const int most = static_cast<int>(kWorkspaceHeader / sizeof(unsigned)) / (a.nt ? 1 : 2);   // counters a CTA: 1 or 2
+  a.ctas = sms * (a.nt == 1 ? (c->head_dim == 64 ? 5 : 4) : (a.nt == 2 ? 3 : (a.nt == 4 ? 2 : 1)));
+  const int most = fp8q::kv4::kMaxCtas;              // of whose counters each CTA has two
   if (a.ctas > most) a.ctas = most;
   const int64_t tile = a.nt ? 8 * a.nt : fp8q::kv4::many::kRows;
   a.row_tiles = static_cast<int>((rows + tile - 1) / tile);
@@ -370,7 +370,7 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
   p.row_tiles = plan.row_tiles;
   if (cache->head_dim == 128) {
-    if (plan.nt == 1) return launch_few<128, 1, 5>(p, plan.ctas, dev, stream);
+    if (plan.nt == 1) return launch_few<128, 1, 4>(p, plan.ctas, dev, stream);
     if (plan.nt == 2) return launch_few<128, 2, 3>(p, plan.ctas, dev, stream);
     if (plan.nt == 4) return launch_few<128, 4, 2>(p, plan.ctas, dev, stream);
     return launch_many<128>(p, plan.ctas, dev, stream);

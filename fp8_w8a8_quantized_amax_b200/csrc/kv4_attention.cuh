@@ -30,6 +30,7 @@ struct AttnParams {
 };
 
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kMaxCtas = 1024;  // counters of each level in the workspace's header
 
 // The rows [r0, r0 + n) and cached tokens of sequence b, bounded to what the
 // tensors hold (a length that has to be cut sets the error word).
@@ -83,6 +84,17 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t (&o)[4]) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// One half of an f16x2 in both halves (the multiplication takes either half of a register by itself).
+__device__ __forceinline__ uint32_t dup_lo(uint32_t a) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t dup_hi(uint32_t a) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(a));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -160,8 +172,10 @@ namespace few {
 
 constexpr int kTile = 32;     // keys of a warp per step
 constexpr int kStages = 2;
+constexpr int kJoin = 16;     // parts of an item joined at a time
 
-// Q fragments in shared memory instead of 16 NT registers: at 32 rows and at 8 (where five CTAs then fit an SM).
+// Q fragments in shared memory instead of 16 NT registers: at 32 rows, and at 8, where the loop then has no spills with
+// four CTAs an SM (five at D = 64; five at D = 128 spilled: 77 us against 70 us for 32 sequences of 8192 keys).
 template <int NT>
 constexpr bool kQInSmem = NT != 2;
 
@@ -282,9 +296,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
   Range range;
   range.q = total / gridDim.x;
   range.r = total - range.q * gridDim.x;
-  const int64_t begin = range.begin(blockIdx.x), end = range.begin(blockIdx.x + 1);
-  if (begin == end) return;
   {
+    const int64_t begin = range.begin(blockIdx.x), end = range.begin(blockIdx.x + 1);
+    if (begin == end) return;
+    // What is needed between jobs only is read back from shared memory there, not held in registers through the loop
+    // over the keys (spills inside that loop cost 10%).
+    if (threadIdx.x == 0) {
+      misc[11] = range.q;
+      misc[12] = range.r;
+    }
     int64_t ahead = 0;
     for (int base = 0; base < p.B; base += L::kThreads) {
       const int64_t all = p.B <= L::kThreads ? total : scan(base);
@@ -351,8 +371,14 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
   uint32_t qf[kQInSmem<NT> ? 1 : NT][kSteps][2];
   // per row: the scores' factor, the base m (negated; 0 before the first key), the score at which it is raised, the sum
   float qscale[NT][2], nbase[NT][2], limit[NT][2], l[NT][2];
-  int pos[NT][2];
   float o[kSteps][NT][4];
+  auto stored_range = [&]() {
+    const volatile int64_t* m = misc;
+    Range r;
+    r.q = m[11];
+    r.r = m[12];
+    return r;
+  };
   int stage = 0, which = 0;
   {
     const Job& j = jobs[0];
@@ -364,21 +390,24 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
 
   for (;; which ^= 1) {
     // ---- an item (or this CTA's part of it): its query rows, and the next job ----
-    const Job& job = jobs[which];
-    const bool more = job.s + job.steps < end;
+    const volatile Job& job = jobs[which];
+    bool more;
+    {
+    const Range range = stored_range();
+    const int64_t end = range.begin(blockIdx.x + 1);
+    more = job.s + job.steps < end;
     if (more && threadIdx.x == 0) {
       const bool whole_item = job.step + job.steps == job.x.steps;       // else this CTA's range ends here
       make_job<kRows, kStep>(p, job.b, job.item + (whole_item ? 1 : 0), 0, job.s + job.steps, end, &jobs[which ^ 1]);
     }
-    const Seq seq = job.x.s;
-    const int hi = job.x.hi, lo = job.x.first, steps = job.steps, item = job.item;
-    const int head = item % p.c.heads, row0 = item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
-    const int32_t* table = p.table + job.b * p.table_stride;
-    int key = job.key + warp * kTile;
-    const uint8_t* codes = codes_of(head);
-    const uint8_t* scales = scales_of(head);
-    int2 page = make_int2(0, 0);
-    if (key + kStep < hi) page = pages_of(table, key + kStep, lo, hi);
+    }
+    const int hi = job.x.hi, lo = job.x.first, steps = job.steps, head = job.item % p.c.heads;
+    int all_first, all_last;                        // keys that every row of the item sees
+    {
+    const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
+    const int row0 = job.item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
+    all_last = visible_last(p, seq, seq.kv - seq.n + row0 / p.group);
+    all_first = visible_first(p, seq.kv - seq.n + (row0 + rows - 1) / p.group);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       // lane (g, t) holds row 8 nt + g, elements [t D/4, (t + 1) D/4)
@@ -421,7 +450,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       qscale[nt][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        pos[nt][i] = seq.kv - seq.n + (row0 + min(nt * 8 + 2 * t + i, rows - 1)) / p.group;
         nbase[nt][i] = 0.0f;
         limit[nt][i] = -INFINITY;
         l[nt][i] = 0.0f;
@@ -431,9 +459,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
     }
-    // keys that every row of the item sees
-    const int all_last = visible_last(p, seq, seq.kv - seq.n + row0 / p.group);
-    const int all_first = visible_first(p, seq.kv - seq.n + (row0 + rows - 1) / p.group);
+    }
+    const int32_t* table = p.table + job.b * p.table_stride;
+    int key = job.key + warp * kTile;
+    const uint8_t* codes = codes_of(head);
+    const uint8_t* scales = scales_of(head);
+    int2 page = make_int2(0, 0);
+    if (key + kStep < hi) page = pages_of(table, key + kStep, lo, hi);
     __syncthreads();                                // jobs[which ^ 1] and the fragments are written
 
     for (int i = 0; i < steps; ++i, key += kStep, stage ^= 1) {
@@ -473,16 +505,16 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
           w1[0] = b.x; w1[1] = b.y; w1[2] = b.z; w1[3] = b.w;
           const uint32_t x = widen_e4m3x2(*reinterpret_cast<const uint16_t*>(ks + r0 * 8 + t * 2));
           const uint32_t y = widen_e4m3x2(*reinterpret_cast<const uint16_t*>(ks + r1 * 8 + t * 2));
-          s0[0] = __byte_perm(x, x, 0x1010); s0[1] = __byte_perm(x, x, 0x3232);
-          s1[0] = __byte_perm(y, y, 0x1010); s1[1] = __byte_perm(y, y, 0x3232);
+          s0[0] = dup_lo(x); s0[1] = dup_hi(x);
+          s1[0] = dup_lo(y); s1[1] = dup_hi(y);
         } else {
           const uint2 a = *reinterpret_cast<const uint2*>(kc + r0 * 32 + t * 8);
           const uint2 b = *reinterpret_cast<const uint2*>(kc + r1 * 32 + t * 8);
           w0[0] = a.x; w0[1] = a.y;
           w1[0] = b.x; w1[1] = b.y;
           const uint32_t x = widen_e4m3x2(ks[r0 * 4 + t] | (static_cast<uint32_t>(ks[r1 * 4 + t]) << 8));
-          s0[0] = s0[1] = __byte_perm(x, x, 0x1010);
-          s1[0] = s1[1] = __byte_perm(x, x, 0x3232);
+          s0[0] = s0[1] = dup_lo(x);
+          s1[0] = s1[1] = dup_hi(x);
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
@@ -519,7 +551,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const int first = visible_first(p, pos[nt][q]), last = visible_last(p, seq, pos[nt][q]);
+            const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
+            const int row0 = job.item / p.c.heads * kRows, end_row = seq.n * p.group - 1;
+            const int pos = seq.kv - seq.n + min(row0 + nt * 8 + 2 * t + q, end_row) / p.group;
+            const int first = visible_first(p, pos), last = visible_last(p, seq, pos);
 #pragma unroll
             for (int mt = 0; mt < kHalves; ++mt)
 #pragma unroll
@@ -651,6 +686,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       }
     }
     __syncthreads();
+    const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
+    const int row0 = job.item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
+    const Range range = stored_range();
+    const int64_t begin = range.begin(blockIdx.x), end = range.begin(blockIdx.x + 1);
     const int64_t i0 = job.s - job.step, i1 = i0 + job.x.steps;      // the item's steps in the list
     const bool split = i0 < begin || i1 > end;
     auto finish = [&](int r, int d, float4 v, float top, float sum) {
@@ -687,64 +726,63 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       }
     }
     if (split) {
-      // the last of the item's CTAs to get here joins their parts in CTA order and leaves the counter zero
+      // The last of the item's CTAs to get here joins their parts, in CTA order, and leaves the counters zero.  Many
+      // parts (a long context of few heads) are joined in two levels: groups of consecutive CTAs first, each by its
+      // last, into its first part's place, then the groups (92 parts of 4 KB by one CTA took 10 us, bound by what one SM
+      // reads from L2).
       const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
-      unsigned* count = p.count + c0;               // an item that goes on past CTA c0's end: one at most
+      const int width = parts <= kJoin ? parts : kJoin;          // parts a group
+      const int groups = (parts + width - 1) / width;
       float* at0 = p.part + (2 * static_cast<int64_t>(c0) + (range.begin(c0) != i0 ? 1 : 0)) * L::kPart;
       float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) misc[10] = atom_add_acq_rel_gpu(count, 1u);
-      __syncthreads();
-      if (static_cast<int>(misc[10]) == parts - 1) {
+      auto part_at = [&](int c) { return c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart; };
+      int from = (static_cast<int>(blockIdx.x) - c0) / width * width, n = min(width, parts - from), stride = 1;
+      unsigned* count = p.count + c0 + from;         // of the group: its first CTA's (an item that goes on past its end: one)
+      for (;;) {
         __threadfence();
-        // Per part a factor exp2(m_c - m), in shared memory (as many parts at a time as fit); then the sums.
-        constexpr int kMost = L::kRedStride;                         // parts: kMost * kRows floats fit one warp's `red`
-        float* red = red_of(0, stage);
-        float4 acc[kRows * (D / 4) / L::kThreads];
-        float tops[kRows * (D / 4) / L::kThreads], sums[kRows * (D / 4) / L::kThreads];
-#pragma unroll
-        for (int u = 0; u < kRows * (D / 4) / L::kThreads; ++u) {
-          acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          tops[u] = -INFINITY;
-          sums[u] = 0.0f;
+        __syncthreads();
+        if (threadIdx.x == 0) misc[10] = atom_add_acq_rel_gpu(count, 1u);
+        __syncthreads();
+        if (static_cast<int>(misc[10]) != n - 1) break;
+        __threadfence();
+        if (threadIdx.x == 0) *count = 0;
+        const bool final = stride > 1 || groups == 1;
+        float* mls = red_of(0, stage);               // the parts' bases and sums
+        for (int i = threadIdx.x; i < n * kRows; i += L::kThreads) {
+          const float* src = part_at(from + i / kRows * stride) + kRows * D + i % kRows;
+          mls[2 * i] = __ldcg(src);
+          mls[2 * i + 1] = __ldcg(src + kRows);
         }
-        for (int p0 = 0; p0 < parts; p0 += kMost / 2) {
-          const int np = min(parts - p0, kMost / 2);
-          __syncthreads();
-          for (int i = threadIdx.x; i < np * kRows; i += L::kThreads) {
-            const int c = p0 + i / kRows, r = i % kRows;
-            const float* src = (c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart) + kRows * D + r;
-            red[2 * i] = __ldcg(src);
-            red[2 * i + 1] = __ldcg(src + kRows);
-          }
-          __syncthreads();
-#pragma unroll
-          for (int u = 0; u < kRows * (D / 4) / L::kThreads; ++u) {
-            const int i = threadIdx.x + u * L::kThreads, r = i / (D / 4);
-            if (r >= rows) continue;
-            float top = tops[u];
-            for (int c = 0; c < np; ++c) top = fmaxf(top, red[2 * (c * kRows + r)]);
-            const float f0 = tops[u] == -INFINITY ? 0.0f : ex2(tops[u] - top);
-            acc[u].x *= f0; acc[u].y *= f0; acc[u].z *= f0; acc[u].w *= f0;
-            sums[u] *= f0;
-            tops[u] = top;
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
+          const int r = i / (D / 4), d = i % (D / 4) * 4;
+          float top = -INFINITY, sum = 0.0f;
+          for (int c = 0; c < n; ++c) top = fmaxf(top, mls[2 * (c * kRows + r)]);
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-            for (int c = 0; c < np; ++c) {
-              const float4* src = reinterpret_cast<const float4*>(p0 + c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(p0 + c - 1) * L::kPart) + i;
-              const float4 x = __ldcg(src);
-              const float mc = red[2 * (c * kRows + r)], f = mc == -INFINITY ? 0.0f : ex2(mc - top);
-              sums[u] += red[2 * (c * kRows + r) + 1] * f;
-              acc[u].x += x.x * f; acc[u].y += x.y * f; acc[u].z += x.z * f; acc[u].w += x.w * f;
+          for (int c = 0; c < n; ++c) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(part_at(from + c * stride)) + i);
+            const float mc = mls[2 * (c * kRows + r)], f = mc == -INFINITY ? 0.0f : ex2(mc - top);
+            sum += mls[2 * (c * kRows + r) + 1] * f;
+            v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+          }
+          if (final) {
+            finish(r, d, v, top, sum);
+          } else {
+            float* dst = part_at(from);
+            __stcg(reinterpret_cast<float4*>(dst) + i, v);
+            if (d == 0) {
+              __stcg(dst + kRows * D + r, top);
+              __stcg(dst + kRows * (D + 1) + r, sum);
             }
           }
         }
-#pragma unroll
-        for (int u = 0; u < kRows * (D / 4) / L::kThreads; ++u) {
-          const int i = threadIdx.x + u * L::kThreads, r = i / (D / 4);
-          if (r < rows) finish(r, i % (D / 4) * 4, acc[u], tops[u], sums[u]);
-        }
-        if (threadIdx.x == 0) *count = 0;
+        if (final) break;
+        from = 0;
+        n = groups;
+        stride = width;
+        count = p.count + kMaxCtas + c0;
+        __syncthreads();                            // misc and mls are free again
       }
     }
     if (!more) break;

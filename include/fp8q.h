@@ -450,7 +450,7 @@ FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* s
  *   A bad length or page index on the device never leads out of the tensors: it
  *   sets the device error word, and the rows concerned are not to be used.
  */
-#define FP8Q_KV4_WORKSPACE_HEADER 4096
+#define FP8Q_KV4_WORKSPACE_HEADER 8192
 FP8Q_API size_t fp8q_kv4_attention_workspace_size(const fp8q_kv4_cache* cache, int64_t B, int64_t T, int64_t Hq,
                                                   int64_t max_q_len);
 FP8Q_API fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, int64_t q_token_stride,
