@@ -365,6 +365,10 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   p.causal = causal;
   p.window = window;
   const AttentionPlan plan = attention_plan(cache, T, Hq, max_q_len, sms);
+  // the kernels count items in 23 bits and steps in 40
+  const int64_t items = B * cache->kv_heads * plan.row_tiles;
+  if (items >= (1 << 22) || items * (max_pages * cache->page_size / 128 + 8) >= (static_cast<int64_t>(1) << 39))
+    return FP8Q_ERR_UNSUPPORTED;
   if (workspace_bytes < plan.bytes()) return FP8Q_ERR_INVALID_ARG;
   p.count = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);

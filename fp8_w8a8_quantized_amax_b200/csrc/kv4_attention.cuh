@@ -62,12 +62,16 @@ __device__ __forceinline__ int visible_last(const AttnParams& p, const Seq& s, i
 }
 
 // The list of all steps of a call, cut evenly over the CTAs.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {     // a >= 0, b > 0; mostly 32-bit values
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 struct Range {
   int64_t q, r;   // CTA c takes q + 1 steps when c < r, else q
   __device__ int64_t begin(int64_t c) const { return c * q + min(c, r); }
   __device__ int owner(int64_t s) const {
     const int64_t big = r * (q + 1);
-    return static_cast<int>(s < big ? s / (q + 1) : r + (s - big) / q);
+    return static_cast<int>(s < big ? quotient(s, q + 1) : r + quotient(s - big, q));
   }
 };
 
@@ -173,6 +177,8 @@ namespace few {
 constexpr int kTile = 32;     // keys of a warp per step
 constexpr int kStages = 2;
 constexpr int kJoin = 16;     // parts of an item joined at a time
+constexpr int kOver = 3;
+constexpr int kJoinCost = 4;  // steps that joining an item's parts takes
 
 // Q fragments in shared memory instead of 16 NT registers: at 32 rows, and at 8, where the loop then has no spills with
 // four CTAs an SM (five at D = 64; five at D = 128 spilled: 77 us against 70 us for 32 sequences of 8192 keys).
@@ -193,7 +199,11 @@ struct Layout {
   static constexpr int kRed = WARPS * kWarpBytes;
   static constexpr int kMl = kRed + (kRedInStage ? 0 : WARPS * kRows * kRedStride * 4);   // [WARPS][kRows] m, then l
   static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // Q fragments, where they are kept in shared memory
-  static constexpr int kMisc = kQ + (kQInSmem<NT> ? NT * (D / 16) * 32 * 8 : 0);
+  // the rows of the current and the next job's queries as they are (bf16), where there is room: at NT = 1
+  static constexpr int kRaw = kQ + (kQInSmem<NT> ? NT * (D / 16) * 32 * 8 : 0);
+  static constexpr bool kQAhead = NT == 1;
+  static constexpr int kRawBytes = kRows * D * 2;
+  static constexpr int kMisc = kRaw + (kQAhead ? 2 * kRawBytes : 0);
   static constexpr int kJobs = kMisc + 128;                        // two jobs of at most 64 bytes
   static constexpr int kBytes = kJobs + 128;
   static constexpr int kPart = kRows * (D + 2);                    // floats of a partial result
@@ -218,8 +228,10 @@ __device__ __forceinline__ Span span(const AttnParams& p, int b) {
   return x;
 }
 
-// A CTA's part of one item: `steps` steps from key `key` on, its number in the
-// list, and what the item is.
+// A CTA's part of one item: `steps` steps from step `step`, key `key` on, its
+// place in the list, and what the item is.
+constexpr int64_t kOneItem = static_cast<int64_t>(1) << 40;
+
 struct Job {
   Span x;
   int b, item, step, steps, key;
@@ -227,8 +239,14 @@ struct Job {
 };
 static_assert(sizeof(Job) <= 64, "two of them in the layout");
 
-// The job that starts at step s of the list, in sequence b, item `item` (both
-// may be one past their end) and step `step`; the CTA's range ends at `end`.
+// The list of steps counts kOver steps more in front of every item: what an
+// item costs beside its keys (its queries, its join), so that the CTAs that get
+// many short items are not the last ones.  A cut that falls into them is a cut
+// ahead of the item's first step.
+//
+// The job of sequence b, item `item` (may be one past the last), step `step`,
+// the item's extra steps starting at s - step - kOver in the list; the CTA's
+// range ends at `end` (steps <= 0: ahead of the job).
 template <int ROWS, int STEP>
 __device__ __forceinline__ void make_job(const AttnParams& p, int b, int item, int step, int64_t s, int64_t end, Job* j) {
   Span x = span<ROWS, STEP>(p, b);
@@ -262,18 +280,22 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
   uint2* qs = reinterpret_cast<uint2*>(smem + L::kQ);
   Job* jobs = reinterpret_cast<Job*>(smem + L::kJobs);             // two: the current one and its successor
   int64_t* misc = reinterpret_cast<int64_t*>(smem + L::kMisc);
+  int* red_max = reinterpret_cast<int*>(misc + 13);
   griddep_wait();
   griddep_launch_dependents();
 
   // ---- this CTA's range of the list: a scan over the sequences' steps ----
-  int64_t total = 0, before = 0;     // before: steps ahead of this thread's sequence, in the last chunk scanned
+  // (steps in the low 40 bits, items above: B items and steps are bounded by the host)
+  int64_t total = 0, before = 0;     // before: what lies ahead of this thread's sequence, in the last chunk scanned
   int64_t mine = 0;
+  int longest = 0;
   auto scan = [&](int base) {
     const int b = base + static_cast<int>(threadIdx.x);
     mine = 0;
     if (b < p.B) {
       const Span x = span<kRows, kStep>(p, b);
-      mine = static_cast<int64_t>(x.items) * x.steps;
+      mine = static_cast<int64_t>(x.items) * (x.steps + kOver + kOneItem);
+      if (x.items > 0) longest = max(longest, x.steps);
     }
     int64_t v = mine;
 #pragma unroll
@@ -294,34 +316,48 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
   };
   for (int base = 0; base < p.B; base += L::kThreads) total += scan(base);
   Range range;
-  range.q = total / gridDim.x;
-  range.r = total - range.q * gridDim.x;
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  if (lane == 0) red_max[warp] = longest;
+  const int items = static_cast<int>(total >> 40);
+  const int64_t steps_all = total & (kOneItem - 1);
+  range.q = quotient(steps_all, gridDim.x);
+  range.r = steps_all - range.q * gridDim.x;
+  __syncthreads();
+  for (int w = 0; w < WARPS; ++w) longest = max(longest, red_max[w]);
+  // As many CTAs as items, or more: each item is left to one of them where its steps take no longer than an even share
+  // and the join (64 sequences of 1000 keys and 8 heads: 28 -> 22 us).
+  const bool by_item = items <= static_cast<int>(gridDim.x) &&
+                       longest + kOver <= max(range.q, static_cast<int64_t>(kOver + 1)) + kJoinCost;
   {
-    const int64_t begin = range.begin(blockIdx.x), end = range.begin(blockIdx.x + 1);
+    const int64_t begin = by_item ? static_cast<int64_t>(blockIdx.x) : range.begin(blockIdx.x);
+    const int64_t end = by_item ? (begin < items ? kOneItem : begin) : range.begin(blockIdx.x + 1);
     if (begin == end) return;
     // What is needed between jobs only is read back from shared memory there, not held in registers through the loop
     // over the keys (spills inside that loop cost 10%).
     if (threadIdx.x == 0) {
-      misc[11] = range.q;
+      misc[11] = by_item ? -1 : range.q;
       misc[12] = range.r;
     }
     int64_t ahead = 0;
     for (int base = 0; base < p.B; base += L::kThreads) {
       const int64_t all = p.B <= L::kThreads ? total : scan(base);
-      if (begin >= ahead && begin < ahead + all) {
-        const int64_t at = begin - ahead - before;
-        if (at >= 0 && at < mine) {
+      const int64_t all_w = by_item ? all >> 40 : all & (kOneItem - 1);
+      if (begin >= ahead && begin < ahead + all_w) {
+        const int64_t at = begin - ahead - (by_item ? before >> 40 : before & (kOneItem - 1));
+        if (at >= 0 && at < (by_item ? mine >> 40 : mine & (kOneItem - 1))) {
           const int b = base + static_cast<int>(threadIdx.x);
-          const int steps = span<kRows, kStep>(p, b).steps;
-          const int item = static_cast<int>(at / steps);
-          make_job<kRows, kStep>(p, b, item, static_cast<int>(at - static_cast<int64_t>(item) * steps), begin, end, jobs);
+          const int steps = span<kRows, kStep>(p, b).steps + kOver;
+          const int item = static_cast<int>(by_item ? at : quotient(at, steps));
+          const int off = by_item ? 0 : static_cast<int>(at - static_cast<int64_t>(item) * steps);
+          make_job<kRows, kStep>(p, b, item, max(0, off - kOver), begin + max(0, kOver - off), end, jobs);
         }
         break;
       }
-      ahead += all;
+      ahead += all_w;
     }
   }
   __syncthreads();
+  if (jobs[0].steps <= 0) return;
 
   // ---- loads: the warp's tile of a step, from one page (two where pages hold 16 keys) ----
   // Nine 16-byte copies a lane at D = 128: four of K's codes, four of V's, one of the scales (lanes 0 .. 15 K's, the
@@ -379,13 +415,36 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
     r.r = m[12];
     return r;
   };
+  auto first_pages = [&](int slot) {                // of a job's first tile
+    const Job& j = jobs[slot];
+    const int k = j.key + warp * kTile;
+    return k < j.x.hi ? pages_of(p.table + j.b * p.table_stride, k, j.x.first, j.x.hi) : make_int2(0, 0);
+  };
+  // A job's query rows, on their way while the job before it is worked on (one group of copies).
+  auto fetch_rows = [&](int slot) {
+    if constexpr (L::kQAhead) {
+      const Job& j = jobs[slot];
+      const int row0 = j.item / p.c.heads * kRows, rows = min(kRows, j.x.s.n * p.group - row0), head = j.item % p.c.heads;
+      for (int i = threadIdx.x; i < rows * (D / 8); i += L::kThreads) {
+        const int r = i / (D / 8), row = row0 + r;
+        cp_async_16(smem + L::kRaw + slot * L::kRawBytes + i * 16,
+                    p.q + (j.x.s.r0 + row / p.group) * p.qt + (head * p.group + row % p.group) * p.qh + i % (D / 8) * 8);
+      }
+      cp_async_commit();
+    }
+  };
   int stage = 0, which = 0;
+  fetch_rows(0);
   {
     const Job& j = jobs[0];
     const int key = j.key + warp * kTile, head = j.item % p.c.heads;
     if (key < j.x.hi)
-      issue(codes_of(head), scales_of(head), pages_of(p.table + j.b * p.table_stride, key, j.x.first, j.x.hi), key, 0);
+      issue(codes_of(head), scales_of(head), first_pages(0), key, 0);
     cp_async_commit();
+  }
+  if constexpr (L::kQAhead) {
+    cp_async_wait<1>();
+    __syncthreads();
   }
 
   for (;; which ^= 1) {
@@ -395,11 +454,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
     {
     const Range range = stored_range();
     const int64_t end = range.begin(blockIdx.x + 1);
-    more = job.s + job.steps < end;
-    if (more && threadIdx.x == 0) {
-      const bool whole_item = job.step + job.steps == job.x.steps;       // else this CTA's range ends here
-      make_job<kRows, kStep>(p, job.b, job.item + (whole_item ? 1 : 0), 0, job.s + job.steps, end, &jobs[which ^ 1]);
-    }
+    more = range.q >= 0 && job.s + job.steps + kOver < end;      // (q < 0: one item a CTA)
+    if (more && threadIdx.x == 0)                    // (then this job ends its item)
+      make_job<kRows, kStep>(p, job.b, job.item + 1, 0, job.s + job.steps + kOver, end, &jobs[which ^ 1]);
     }
     const int hi = job.x.hi, lo = job.x.first, steps = job.steps, head = job.item % p.c.heads;
     int all_first, all_last;                        // keys that every row of the item sees
@@ -414,8 +471,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       const int r = nt * 8 + g;
       uint32_t w[D / 8];
       if (r < rows) {
-        const uint16_t* src = p.q + (seq.r0 + (row0 + r) / p.group) * p.qt +
-                              (head * p.group + (row0 + r) % p.group) * p.qh + t * (D / 4);
+        const uint16_t* src;
+        if constexpr (L::kQAhead)
+          src = reinterpret_cast<const uint16_t*>(smem + L::kRaw + which * L::kRawBytes) + r * D + t * (D / 4);
+        else
+          src = p.q + (seq.r0 + (row0 + r) / p.group) * p.qt + (head * p.group + (row0 + r) % p.group) * p.qh + t * (D / 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -464,24 +524,31 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
     int key = job.key + warp * kTile;
     const uint8_t* codes = codes_of(head);
     const uint8_t* scales = scales_of(head);
-    int2 page = make_int2(0, 0);
+    int2 page = make_int2(0, 0);                    // of the tile to fetch next
     if (key + kStep < hi) page = pages_of(table, key + kStep, lo, hi);
     __syncthreads();                                // jobs[which ^ 1] and the fragments are written
+    if (more) {
+      fetch_rows(which ^ 1);
+      if (steps == 1) page = first_pages(which ^ 1);
+    }
 
     for (int i = 0; i < steps; ++i, key += kStep, stage ^= 1) {
       // ---- the next step's tile goes on its way ----
       if (i + 1 < steps) {
         if (key + kStep < hi) issue(codes, scales, page, key + kStep, stage ^ 1);
-        if (key + 2 * kStep < hi) page = pages_of(table, key + 2 * kStep, lo, hi);
+        if (i + 2 < steps) {
+          if (key + 2 * kStep < hi) page = pages_of(table, key + 2 * kStep, lo, hi);
+        } else if (more) {
+          page = first_pages(which ^ 1);
+        }
       } else if (more) {
         const Job& j = jobs[which ^ 1];
         const int k = j.key + warp * kTile, h = j.item % p.c.heads;
-        if (k < j.x.hi)
-          issue(codes_of(h), scales_of(h), pages_of(p.table + j.b * p.table_stride, k, j.x.first, j.x.hi), k, stage ^ 1);
+        if (k < j.x.hi) issue(codes_of(h), scales_of(h), page, k, stage ^ 1);
       }
       cp_async_commit();                            // one group a step, empty or not
+      cp_async_wait<1>();                           // all but the next step's
       if (key >= hi) continue;
-      cp_async_wait<1>();
       __syncwarp();                                 // the other lanes' copies too
       const uint8_t* kc = stages + stage * L::kStageBytes;
       const uint8_t* ks = kc + L::kCodes;
@@ -689,9 +756,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
     const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
     const int row0 = job.item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
     const Range range = stored_range();
-    const int64_t begin = range.begin(blockIdx.x), end = range.begin(blockIdx.x + 1);
     const int64_t i0 = job.s - job.step, i1 = i0 + job.x.steps;      // the item's steps in the list
-    const bool split = i0 < begin || i1 > end;
+    const bool split = job.steps < job.x.steps;
     auto finish = [&](int r, int d, float4 v, float top, float sum) {
       const int row = row0 + r;
       const int64_t token = seq.r0 + row / p.group;
@@ -703,7 +769,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       *reinterpret_cast<uint2*>(p.o + token * p.ot + h * p.oh + d) = w;
       if (p.lse && d == 0) p.lse[token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
     };
-    float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.s == begin ? 0 : 1)) * L::kPart;
+    float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.step > 0 ? 0 : 1)) * L::kPart;   // a CTA's first job, its last
     for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float top = -INFINITY, sum = 0.0f;
@@ -733,7 +799,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
       const int width = parts <= kJoin ? parts : kJoin;          // parts a group
       const int groups = (parts + width - 1) / width;
-      float* at0 = p.part + (2 * static_cast<int64_t>(c0) + (range.begin(c0) != i0 ? 1 : 0)) * L::kPart;
+      float* at0 = p.part + (2 * static_cast<int64_t>(c0) + 1) * L::kPart;
       float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
       auto part_at = [&](int c) { return c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart; };
       int from = (static_cast<int>(blockIdx.x) - c0) / width * width, n = min(width, parts - from), stride = 1;
