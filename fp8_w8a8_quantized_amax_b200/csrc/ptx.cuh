@@ -153,6 +153,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 
+// The same for hand-overs that are due at once: polls for a while before it suspends (a suspended wait resumes late).
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, volatile int* abort, int site) {
+  const uint32_t b = smem_u32(bar);
+  for (int i = 0; i < 64; ++i)
+    if (mbar_test_wait(b, parity)) return true;
+  return mbar_wait(bar, parity, abort, site);
+}
+
 // After an abort: wait for a phase that completes on its own (a TMA load or
 // MMAs already issued), so that nothing is still writing the CTA's shared or
 // tensor memory when it is released.  The abort flag is ignored; the time
