@@ -71,6 +71,10 @@ __device__ __forceinline__ Unit unit_of(const AttnParams& p, int u) {
   return x;
 }
 
+// The lists of steps count kOver steps more in front of every item, as in the
+// kernel for few rows: here an item's pipeline fills and its sums are written.
+constexpr int kOver = 2;
+
 struct Job {
   Unit x;
   int u, head, step, steps;
@@ -78,16 +82,33 @@ struct Job {
 };
 static_assert(sizeof(Job) <= 64, "the layout's job list");
 
-// Column c of the softmax's view: keys outside [first, last) of the row count as minus infinity.
-template <bool MASK>
-__device__ __forceinline__ float masked(uint32_t v, int c, int first, int last) {
-  const float f = __uint_as_float(v);
-  return !MASK || (c >= first && c < last) ? f : -INFINITY;
+__device__ __forceinline__ void make_job(const Unit& x, int u, int head, int step, int64_t s, int64_t end, Job* j) {
+  j->x = x;
+  j->u = u;
+  j->head = head;
+  j->step = step;
+  j->steps = static_cast<int>(min(static_cast<int64_t>(x.steps - step), end - s));
+  j->s = s;
+}
+
+// Keys outside [first, last) of a row of S become minus infinity (the first and last tiles of an item only, so apart:
+// the two passes below are then compiled once).
+__device__ __forceinline__ void row_mask(uint32_t ts, int first, int last) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(ts + 32 * c, r);
+    tmem_ld_wait_regs(r);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (32 * c + i < first || 32 * c + i >= last) r[i] = 0xFF800000u;
+    tmem_st_32x32b_x32(ts + 32 * c, r);
+  }
+  tmem_st_wait();
 }
 
 // Both passes over a row of S work on 32 columns while the next 32 are on their way from tensor memory.
-template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t ts, int first, int last) {
+__device__ __forceinline__ float row_max(uint32_t ts) {
   float top[2] = {-INFINITY, -INFINITY};
   uint32_t r[2][32];
   tmem_ld_32x32b_x32(ts, r[0]);
@@ -97,15 +118,13 @@ __device__ __forceinline__ float row_max(uint32_t ts, int first, int last) {
     if (c < 3) tmem_ld_32x32b_x32(ts + 32 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
     for (int i = 0; i < 32; i += 2)
-      top[i / 2 & 1] = fmaxf(top[i / 2 & 1], fmaxf(masked<MASK>(r[c & 1][i], 32 * c + i, first, last),
-                                                   masked<MASK>(r[c & 1][i + 1], 32 * c + i + 1, first, last)));
+      top[i / 2 & 1] = fmaxf(top[i / 2 & 1], fmaxf(__uint_as_float(r[c & 1][i]), __uint_as_float(r[c & 1][i + 1])));
   }
   return fmaxf(top[0], top[1]);
 }
 
 // P = 2^(S qscale + nbase) in f16 over S; returns the sum.
-template <bool MASK>
-__device__ __forceinline__ float row_exp(uint32_t ts, int first, int last, float qscale, float nbase) {
+__device__ __forceinline__ float row_exp(uint32_t ts, float qscale, float nbase) {
   const uint64_t scale2 = f32x2_pack(qscale, qscale), base2 = f32x2_pack(nbase, nbase);
   uint64_t sum2[2] = {f32x2_pack(0.0f, 0.0f), f32x2_pack(0.0f, 0.0f)};
   uint32_t r[2][32];
@@ -117,8 +136,7 @@ __device__ __forceinline__ float row_exp(uint32_t ts, int first, int last, float
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float x = masked<MASK>(r[c & 1][2 * i], 32 * c + 2 * i, first, last);
-      float y = masked<MASK>(r[c & 1][2 * i + 1], 32 * c + 2 * i + 1, first, last);
+      float x = __uint_as_float(r[c & 1][2 * i]), y = __uint_as_float(r[c & 1][2 * i + 1]);
       f32x2_unpack(fma_f32x2(f32x2_pack(x, y), scale2, base2), x, y);
       x = ex2(x);
       y = ex2(y);
@@ -147,12 +165,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   Job* jobs = reinterpret_cast<Job*>(smem + L::kJobOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t *q_full = bars, *s_full = bars + 2, *p_full = bars + 4, *o_full = bars + 6;
-  uint64_t *k_full = bars + 8, *k_empty = bars + 10, *v_full = bars + 12, *v_empty = bars + 14, *drain = bars + 16, *join = bars + 17;
-  int64_t* misc = reinterpret_cast<int64_t*>(smem + L::kBar + 176);     // 16 warps' sums, the first job's unit and place
+  uint64_t *k_full = bars + 8, *k_empty = bars + 10, *v_full = bars + 12, *v_empty = bars + 14, *drain = bars + 16;
+  int64_t* misc = reinterpret_cast<int64_t*>(smem + L::kBar + 176);     // the warps' sums
   int* flags = reinterpret_cast<int*>(smem + L::kBar + 176 + 18 * 8);
   volatile int* abort = flags;
   int* njobs = flags + 1;
-  int* last_one = flags + 2;                        // two
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(flags + 4);
   float* qscales = reinterpret_cast<float*>(smem + L::kScaleOff);
   const int warp = threadIdx.x >> 5, lane = lane_id();
@@ -168,7 +185,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 4);
       mbar_init(&v_empty[i], 1);
-      mbar_init(&join[i], 4);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -182,7 +198,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   int64_t total = 0, before = 0, mine = 0;
   auto scan = [&](int base) {
     const int u = base + static_cast<int>(threadIdx.x);
-    mine = u < units ? static_cast<int64_t>(unit_of(p, u).steps) * p.c.heads : 0;
+    mine = 0;
+    if (u < units) {
+      const int steps = unit_of(p, u).steps;
+      if (steps > 0) mine = static_cast<int64_t>(steps + kOver) * p.c.heads;
+    }
     int64_t v = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -202,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   };
   for (int base = 0; base < units; base += kThreads) total += scan(base);
   Range range;
-  range.q = total / gridDim.x;
+  range.q = quotient(total, gridDim.x);
   range.r = total - range.q * gridDim.x;
   const int64_t begin = range.begin(blockIdx.x), end = range.begin(blockIdx.x + 1);
   if (begin == end) return;
@@ -216,9 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const int64_t all = units <= kThreads ? total : scan(base);
       if (begin >= ahead && begin < ahead + all) {
         const int64_t at = begin - ahead - before;
-        if (at >= 0 && at < mine) {
-          misc[16] = base + static_cast<int>(threadIdx.x);
-          misc[17] = at;
+        if (at >= 0 && at < mine) {                  // the first job is this thread's
+          const int u = base + static_cast<int>(threadIdx.x);
+          const Unit x = unit_of(p, u);
+          const int head = static_cast<int>(quotient(at, x.steps + kOver)), off = static_cast<int>(at - static_cast<int64_t>(head) * (x.steps + kOver));
+          make_job(x, u, head, max(0, off - kOver), begin + max(0, kOver - off), end, jobs);
         }
         break;
       }
@@ -229,60 +251,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const bool none = jobs[0].steps <= 0;              // the range lies ahead of an item's first step
 
   // counts of what a role has waited for, over all jobs
   int tiles = 0;                 // key tiles (widening warps, product warp)
   int turns = 0, done = 0;       // softmax: S tiles, items; product warp: the first tile's
-  int meets = 0;                 // softmax: meetings of a tile's threads
   int turns1 = 0, done1 = 0;     // product warp: the second tile's
-  // The jobs of a CTA are listed kJobs at a time; every role walks through the list by itself, and all meet in between.
-  int64_t next_s = begin;
+  // The jobs of a CTA are listed kJobs at a time.  The first of a list stands before the roles begin with it; the
+  // others are listed meanwhile by the product warp.  Every role walks through the list by itself.
   auto meet_all = []() {
     __syncwarp();
     asm volatile("bar.sync 0;" ::: "memory");
   };
-  auto list_done = [&](int n) {                     // every role is through the list: whether there is no other
-    __syncwarp();
-    next_s = jobs[n - 1].s + jobs[n - 1].steps;
-    meet_all();
-    return next_s >= end || *abort;
+  // the job after `j`, if the range reaches it (j then ends its item)
+  auto job_after = [&](const Job& j, Job* to) {
+    Unit x = j.x;
+    int u = j.u, head = j.head + 1;
+    const int64_t s = j.s + j.steps + kOver;
+    if (s >= end) return false;
+    while ((head >= p.c.heads || x.rows == 0) && u + 1 < units) {
+      head = 0;
+      x = unit_of(p, ++u);
+    }
+    make_job(x, u, head, 0, s, end, to);
+    return true;
   };
-  if (warp < 8) {
+  auto list_jobs = [&]() {                           // one thread, after jobs[0]
+    int n = 1;
+    while (n < kJobs && job_after(jobs[n - 1], &jobs[n])) ++n;
+    *njobs = n;
+  };
+  auto list_done = [&](int n) {                     // every role is through the list: whether there is no other
+    meet_all();
+    const Job last = jobs[n - 1];
+    const bool over = last.s + last.steps + kOver >= end || *abort;
+    if (over) return true;
+    meet_all();
+    if (threadIdx.x == 12 * 32) job_after(last, &jobs[0]);
+    meet_all();
+    return false;
+  };
+  if (none) {
+  } else if (warp < 8) {
     for (;;) {
-      if (lane == 0) {
-        int n = 0;
-        int u, head, step;
-        if (next_s == begin) {
-          u = static_cast<int>(misc[16]);
-          const int steps = unit_of(p, u).steps;
-          head = static_cast<int>(misc[17] / steps);
-          step = static_cast<int>(misc[17] - static_cast<int64_t>(head) * steps);
-        } else {
-          u = jobs[kJobs - 1].u;
-          head = jobs[kJobs - 1].head + 1;             // a job that is not the last one ends its item
-          step = 0;
-        }
-        Unit x = unit_of(p, u);
-        int64_t s = next_s;
-        while (n < kJobs && s < end) {
-          while ((head >= p.c.heads || x.rows == 0) && u + 1 < units) {
-            head = 0;
-            x = unit_of(p, ++u);
-          }
-          Job& j = jobs[n++];
-          j.x = x;
-          j.u = u;
-          j.head = head++;
-          j.step = step;
-          j.steps = static_cast<int>(min(static_cast<int64_t>(x.steps - step), end - s));
-          j.s = s;
-          s += j.steps;
-          step = 0;
-        }
-        *njobs = n;
-      }
-      meet_all();
-      const int n = *njobs;
         // ----------------------------------------------------------- softmax ---
         const int w = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // 32 lanes a warp
@@ -293,13 +304,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
           const int c = lane % kLanes, first = (warp & 3) * 32 + lane / kLanes;
           uint4 v[kLanes];
+          const int row = job.x.row0 + w * 128 + first, dt = kAtOnce / p.group, dh = kAtOnce - dt * p.group;
+          int t = row / p.group, h = row - t * p.group;
+          const uint16_t* src = p.q + static_cast<int64_t>(job.x.s.r0) * p.qt + static_cast<int64_t>(job.head) * p.group * p.qh + 8 * c;
 #pragma unroll
           for (int u = 0; u < kLanes; ++u) {
-            const int r = first + u * kAtOnce, row = job.x.row0 + w * 128 + r;
             v[u] = make_uint4(0, 0, 0, 0);
-            if (w * 128 + r < job.x.rows)
-              v[u] = *reinterpret_cast<const uint4*>(p.q + (job.x.s.r0 + static_cast<int64_t>(row / p.group)) * p.qt +
-                                                     (job.head * p.group + row % p.group) * p.qh + 8 * c);
+            if (w * 128 + first + u * kAtOnce < job.x.rows) v[u] = *reinterpret_cast<const uint4*>(src + t * p.qt + h * p.qh);
+            t += dt;
+            h += dh;
+            if (h >= p.group) {
+              h -= p.group;
+              ++t;
+            }
           }
 #pragma unroll
           for (int u = 0; u < kLanes; ++u) {
@@ -322,13 +339,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           fence_proxy_async_smem();
           warp_arrive(&q_full[w]);
         };
+        const bool first_mine = w * 128 < jobs[0].x.rows;
+        if (first_mine) bring_queries(jobs[0]);
+        meet_all();
+        const int n = *njobs;
         auto next_job = [&](int i) {                 // the next item with rows of this tile
           while (i < n && w * 128 >= jobs[i].x.rows) ++i;
           return i;
         };
         bool ok = true;
         int i = next_job(0);
-        if (i < n) bring_queries(jobs[i]);
+        if (!first_mine && i < n) bring_queries(jobs[i]);
         for (int following; i < n && ok; i = following) {
           const Job& job = jobs[i];
           const Unit x = job.x;
@@ -351,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
               continue;
             }
             const int first = vfirst - key, last = vlast - key;
-            const bool whole = __all_sync(0xFFFFFFFFu, first <= 0 && last >= kKeys);
-            const float top = whole ? row_max<false>(ts, 0, 0) : row_max<true>(ts, first, last);
+            if (!__all_sync(0xFFFFFFFFu, first <= 0 && last >= kKeys)) row_mask(ts, first, last);
+            const float top = row_max(ts);
             if (__any_sync(0xFFFFFFFFu, top > limit)) {
               const float was = limit == -INFINITY ? -INFINITY : -nbase, now = fmaxf(was, top * qscale);
               float f = 1.0f;
@@ -374,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 }
               }
             }
-            sum += whole ? row_exp<false>(ts, 0, 0, qscale, nbase) : row_exp<true>(ts, first, last, qscale, nbase);
+            sum += row_exp(ts, qscale, nbase);
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&p_full[w]);
@@ -387,11 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           ++done;
           tc_fence_after();
           // ---- the item's end ----
-          const int64_t i0 = job.s - job.step, i1 = i0 + x.steps;
           const float top = limit == -INFINITY ? -INFINITY : -nbase;
           const int64_t out_token = x.s.r0 + static_cast<int64_t>(token);
           uint16_t* out = p.o + out_token * p.ot + h * p.oh;
-          if (i0 >= begin && i1 <= end) {
+          if (job.steps == x.steps) {
             const float f = sum > 0.0f ? p.c.vg / sum : 0.0f;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -413,9 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             if (p.lse && real) p.lse[out_token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
             tc_fence_before();
           } else {
-            // a part: [D / 4][256] float4 (coalesced over the rows), the bases, the sums
+            // A part: [D / 4][256] float4 (coalesced over the rows), the bases, the sums.  Every warp joins its own 32
+            // rows: the last CTA's warp to get here, in CTA order.
+            const int64_t i0 = job.s - job.step, i1 = i0 + x.steps;      // the item's steps in the list
             const int row_in = w * 128 + r;
-            float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.s == begin ? 0 : 1)) * L::kPart;
+            float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.step > 0 ? 0 : 1)) * L::kPart;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -431,52 +453,57 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             __stcg(slot + kRows * D + row_in, top);
             __stcg(slot + kRows * (D + 1) + row_in, sum);
             const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
-            // a tile's 128 threads meet at an mbarrier: its wait is bounded, so that none waits for one that gave up
-            auto meet = [&]() {
-              warp_arrive(&join[w]);
-              return mbar_wait(&join[w], meets++ & 1, abort, kErrWaitEmpty);
-            };
+            unsigned* count = p.count + c0 * 8 + warp;
             __threadfence();
-            if (!(ok = meet())) break;
-            if (r == 0) last_one[w] = atom_add_acq_rel_gpu(p.count + 2 * c0 + w, 1u) == static_cast<unsigned>(parts - 1);
-            if (!(ok = meet())) break;
-            if (last_one[w]) {
+            __syncwarp();
+            unsigned arrived = 0;
+            if (lane == 0) arrived = atom_add_acq_rel_gpu(count, 1u);
+            arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
+            if (arrived == static_cast<unsigned>(parts - 1)) {
               __threadfence();
-              const float* at0 = p.part + (2 * static_cast<int64_t>(c0) + (range.begin(c0) != i0 ? 1 : 0)) * L::kPart;
+              if (lane == 0) *count = 0;
+              const float* at0 = p.part + (2 * static_cast<int64_t>(c0) + 1) * L::kPart;
               const float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
               auto part = [&](int c) { return c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart; };
               float m = -INFINITY, l = 0.0f;
               for (int c = 0; c < parts; ++c) m = fmaxf(m, __ldcg(part(c) + kRows * D + row_in));
-              for (int c = 0; c < parts; ++c) {
+              auto share = [&](int c) {              // a part's factor
                 const float mc = __ldcg(part(c) + kRows * D + row_in);
-                if (mc != -INFINITY) l += __ldcg(part(c) + kRows * (D + 1) + row_in) * ex2(mc - m);
-              }
+                return mc == -INFINITY ? 0.0f : ex2(mc - m);
+              };
+              for (int c = 0; c < parts; ++c) l += __ldcg(part(c) + kRows * (D + 1) + row_in) * share(c);
               const float f = l > 0.0f ? p.c.vg / l : 0.0f;
-              for (int e = 0; e < D / 8; ++e) {
-                float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+#pragma unroll
+              for (int e = 0; e < D / 32; ++e) {     // 32 columns: eight loads on their way
+                float4 a[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 for (int c = 0; c < parts; ++c) {
-                  const float mc = __ldcg(part(c) + kRows * D + row_in), g = mc == -INFINITY ? 0.0f : ex2(mc - m);
-                  const float4 u = __ldcg(reinterpret_cast<const float4*>(part(c)) + 2 * e * kRows + row_in);
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(part(c)) + (2 * e + 1) * kRows + row_in);
-                  a.x += u.x * g; a.y += u.y * g; a.z += u.z * g; a.w += u.w * g;
-                  b.x += v.x * g; b.y += v.y * g; b.z += v.z * g; b.w += v.w * g;
+                  float4 v[8];
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(part(c)) + (8 * e + k) * kRows + row_in);
+                  const float g = share(c);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) {
+                    a[k].x += v[k].x * g; a[k].y += v[k].y * g; a[k].z += v[k].z * g; a[k].w += v[k].w * g;
+                  }
                 }
-                if (real)
-                  *reinterpret_cast<uint4*>(out + 8 * e) = make_uint4(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f),
-                                                                      pack_bf16x2(b.x * f, b.y * f), pack_bf16x2(b.z * f, b.w * f));
+                if (real) {
+#pragma unroll
+                  for (int k = 0; k < 8; k += 2)
+                    *reinterpret_cast<uint4*>(out + 32 * e + 4 * k) =
+                        make_uint4(pack_bf16x2(a[k].x * f, a[k].y * f), pack_bf16x2(a[k].z * f, a[k].w * f),
+                                   pack_bf16x2(a[k + 1].x * f, a[k + 1].y * f), pack_bf16x2(a[k + 1].z * f, a[k + 1].w * f));
+                }
               }
               if (p.lse && real) p.lse[out_token * p.Hq + h] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
-              if (r == 0) p.count[2 * c0 + w] = 0;
             }
-            if (!(ok = meet())) break;                 // last_one is free again
           }
         }
       if (list_done(n)) break;
     }
   } else if (warp < 12) {
     for (;;) {
-      meet_all();
-      const int n = *njobs;
         // ---------------------------------------------------------- widening ---
         // One thread per key; the next tile's bytes are on their way while this one's are widened.
         const int r = threadIdx.x - 256;
@@ -535,6 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         int page = page_of(jobs[0], 0);
         fetch(jobs[0], 0, page, 0);
         fetch(jobs[0], 0, page, 1);
+        meet_all();
+        const int n = *njobs;
         step_on(fi, fj);
         page = fi < n ? page_of(jobs[fi], fj) : -1;
         for (int i = 0; i < n && ok; ++i) {
@@ -560,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (list_done(n)) break;
     }
   } else {
-  if (warp == 12) {
     for (;;) {
+      if (lane == 0) list_jobs();
       meet_all();
       const int n = *njobs;
         // ---------------------------------------------------------- products ---
@@ -625,7 +654,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
       if (list_done(n)) break;
     }
-  }
   }
   // After a wait that ran out, what the tensor cores still work on ends before their memory is given back.
   if (*abort && warp == 12) {
