@@ -123,6 +123,33 @@ __device__ __forceinline__ float row_max(uint32_t ts) {
   return fmaxf(top[0], top[1]);
 }
 
+// 2^z for two values on the FMA pipes: z = n + r, |r| <= 1/2, a polynomial of degree 5 in r (least maximal relative error,
+// 2^-22; fitted on a grid by repeated weighted least squares), and n added to the exponent.  z is held at -126 from
+// below, so minus infinity becomes 2^-126, an f16 zero.
+__device__ __forceinline__ void exp2_poly(uint64_t z2, float& x, float& y) {
+  f32x2_unpack(z2, x, y);
+  const uint64_t z = f32x2_pack(fmaxf(x, -126.0f), fmaxf(y, -126.0f));
+  const uint64_t magic = f32x2_pack(12582912.0f, 12582912.0f), minus = f32x2_pack(-12582912.0f, -12582912.0f);
+  const uint64_t t = add_f32x2(z, magic);            // 1.5 2^23 + n: n in the low bits
+  const uint64_t n = add_f32x2(t, minus);
+  const uint64_t r = fma_f32x2(n, f32x2_pack(-1.0f, -1.0f), z);
+  uint64_t q = f32x2_pack(0.001327647129073739f, 0.001327647129073739f);
+  q = fma_f32x2(q, r, f32x2_pack(0.009675540961325169f, 0.009675540961325169f));
+  q = fma_f32x2(q, r, f32x2_pack(0.05550713092088699f, 0.05550713092088699f));
+  q = fma_f32x2(q, r, f32x2_pack(0.24022120237350464f, 0.24022120237350464f));
+  q = fma_f32x2(q, r, f32x2_pack(0.6931469440460205f, 0.6931469440460205f));
+  q = fma_f32x2(q, r, f32x2_pack(1.0000001192092896f, 1.0000001192092896f));
+  float qx, qy, tx, ty;
+  f32x2_unpack(q, qx, qy);
+  f32x2_unpack(t, tx, ty);
+  x = __uint_as_float(__float_as_uint(tx) * 8388608u + __float_as_uint(qx));
+  y = __uint_as_float(__float_as_uint(ty) * 8388608u + __float_as_uint(qy));
+}
+
+// One pair in kPoly is raised on the FMA pipes, the others by the function unit, which by itself would take half the
+// softmax's time.
+constexpr int kPoly = 6;
+
 // P = 2^(S qscale + nbase) in f16 over S; returns the sum.
 __device__ __forceinline__ float row_exp(uint32_t ts, float qscale, float nbase) {
   const uint64_t scale2 = f32x2_pack(qscale, qscale), base2 = f32x2_pack(nbase, nbase);
@@ -137,9 +164,14 @@ __device__ __forceinline__ float row_exp(uint32_t ts, float qscale, float nbase)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float x = __uint_as_float(r[c & 1][2 * i]), y = __uint_as_float(r[c & 1][2 * i + 1]);
-      f32x2_unpack(fma_f32x2(f32x2_pack(x, y), scale2, base2), x, y);
-      x = ex2(x);
-      y = ex2(y);
+      const uint64_t z = fma_f32x2(f32x2_pack(x, y), scale2, base2);
+      if (i % kPoly == kPoly - 1) {
+        exp2_poly(z, x, y);
+      } else {
+        f32x2_unpack(z, x, y);
+        x = ex2(x);
+        y = ex2(y);
+      }
       sum2[i & 1] = add_f32x2(sum2[i & 1], f32x2_pack(x, y));
       w[i] = pack_f16x2(x, y);
     }
@@ -247,11 +279,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       ahead += all;
     }
   }
+  if (threadIdx.x == 0) {
+    misc[16] = range.q;
+    misc[17] = range.r;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool none = jobs[0].steps <= 0;              // the range lies ahead of an item's first step
+  // What a role needs between items only is read back from shared memory there, not held in registers.
+  const volatile int64_t* kept = misc;               // range.q, range.r
+  auto range_end = [&]() {
+    Range k;
+    k.q = kept[16];
+    k.r = kept[17];
+    return k.begin(blockIdx.x + 1);
+  };
 
   // counts of what a role has waited for, over all jobs
   int tiles = 0;                 // key tiles (widening warps, product warp)
@@ -267,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   auto job_after = [&](const Job& j, Job* to) {
     Unit x = j.x;
     int u = j.u, head = j.head + 1;
-    const int64_t s = j.s + j.steps + kOver;
+    const int64_t s = j.s + j.steps + kOver, end = range_end();
     if (s >= end) return false;
     while ((head >= p.c.heads || x.rows == 0) && u + 1 < units) {
       head = 0;
@@ -284,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   auto list_done = [&](int n) {                     // every role is through the list: whether there is no other
     meet_all();
     const Job last = jobs[n - 1];
-    const bool over = last.s + last.steps + kOver >= end || *abort;
+    const bool over = last.s + last.steps + kOver >= range_end() || *abort;
     if (over) return true;
     meet_all();
     if (threadIdx.x == 12 * 32) job_after(last, &jobs[0]);
@@ -351,18 +395,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         int i = next_job(0);
         if (!first_mine && i < n) bring_queries(jobs[i]);
         for (int following; i < n && ok; i = following) {
-          const Job& job = jobs[i];
-          const Unit x = job.x;
+          const volatile Job& job = jobs[i];
           following = next_job(i + 1);
-          const int row = x.row0 + w * 128 + r;
-          const bool real = w * 128 + r < x.rows, idle = w * 128 + (r & ~31) >= x.rows;
-          const int token = min(row, x.row0 + x.rows - 1) / p.group, pos = x.s.kv - x.s.n + token;
-          const int h = job.head * p.group + row - row / p.group * p.group;
           const float qscale = qscales[w * 128 + r];   // (written by this warp)
-          const int vfirst = visible_first(p, pos), vlast = visible_last(p, x.s, pos);
+          const bool idle = w * 128 + (r & ~31) >= job.x.rows;
+          int vfirst, vlast;
+          {
+            const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
+            const int pos = seq.kv - seq.n + (job.x.row0 + min(w * 128 + r, job.x.rows - 1)) / p.group;
+            vfirst = visible_first(p, pos);
+            vlast = visible_last(p, seq, pos);
+          }
           float nbase = 0.0f, limit = -INFINITY, sum = 0.0f;
-          int key = x.lo + job.step * kKeys;
-          for (int j = 0; j < job.steps; ++j, key += kKeys, ++turns) {
+          int key = job.x.lo + job.step * kKeys;
+          const int steps = job.steps;
+          for (int j = 0; j < steps; ++j, key += kKeys, ++turns) {
             ok = mbar_spin(&s_full[w], turns & 1, abort, kErrWaitTmemFull);
             if (!ok) break;
             tc_fence_after();
@@ -409,9 +456,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           tc_fence_after();
           // ---- the item's end ----
           const float top = limit == -INFINITY ? -INFINITY : -nbase;
-          const int64_t out_token = x.s.r0 + static_cast<int64_t>(token);
+          if (limit == -INFINITY) sum = 0.0f;        // no visible key (the polynomial's least value is not zero)
+          const bool real = w * 128 + r < job.x.rows;
+          const int row = job.x.row0 + w * 128 + r, token = row / p.group, h = job.head * p.group + row - token * p.group;
+          const int64_t out_token = job.x.s.r0 + static_cast<int64_t>(token);
           uint16_t* out = p.o + out_token * p.ot + h * p.oh;
-          if (job.steps == x.steps) {
+          if (job.steps == job.x.steps) {
             const float f = sum > 0.0f ? p.c.vg / sum : 0.0f;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -435,7 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           } else {
             // A part: [D / 4][256] float4 (coalesced over the rows), the bases, the sums.  Every warp joins its own 32
             // rows: the last CTA's warp to get here, in CTA order.
-            const int64_t i0 = job.s - job.step, i1 = i0 + x.steps;      // the item's steps in the list
+            const int64_t i0 = job.s - job.step, i1 = i0 + job.x.steps;  // the item's steps in the list
+            Range range;
+            range.q = kept[16];
+            range.r = kept[17];
             const int row_in = w * 128 + r;
             float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.step > 0 ? 0 : 1)) * L::kPart;
 #pragma unroll
@@ -466,11 +519,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
               const float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
               auto part = [&](int c) { return c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart; };
               float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
               for (int c = 0; c < parts; ++c) m = fmaxf(m, __ldcg(part(c) + kRows * D + row_in));
               auto share = [&](int c) {              // a part's factor
                 const float mc = __ldcg(part(c) + kRows * D + row_in);
                 return mc == -INFINITY ? 0.0f : ex2(mc - m);
               };
+#pragma unroll 4
               for (int c = 0; c < parts; ++c) l += __ldcg(part(c) + kRows * (D + 1) + row_in) * share(c);
               const float f = l > 0.0f ? p.c.vg / l : 0.0f;
 #pragma unroll
@@ -478,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 float4 a[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
                 for (int c = 0; c < parts; ++c) {
                   float4 v[8];
 #pragma unroll
