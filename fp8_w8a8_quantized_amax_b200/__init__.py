@@ -397,51 +397,56 @@ class _CacheStruct(ctypes.Structure):
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
-def _call(dev: int, name: str, *args) -> None:
-    """lib().<name>(*args, the current stream of device `dev`) with that device current; raises on an error status."""
-    f = getattr(lib(), name)
-    if dev == torch.cuda.current_device():
-        st = f(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = f(*args, _raw_stream(dev))
-    if st != OK:
-        raise FP8QError(st, name)
-
-
 def _raw_stream(dev: int) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):      # the same handle without a Stream object
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+def _current_device() -> int:
+    return torch.cuda.current_device()
 
 
-def _require_heads(t: torch.Tensor, name: str, dev: int, shape=None) -> None:
-    """A bf16 tensor [tokens, heads, head_dim] with contiguous elements on CUDA device `dev`."""
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{dev}" if dev >= 0 else ""))
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be bf16, got {t.dtype}")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with unit stride in the last dimension")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+# The same values without a Stream object and a check for initialisation (the operands are CUDA tensors by then).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", _current_device)
 
 
-def _head_strides(t: torch.Tensor, T: int, H: int, D: int) -> Tuple[int, int]:
-    """(token, head) strides; those of dimensions of size 1 as in a contiguous tensor."""
-    return (t.stride(0) if T > 1 else H * D), (t.stride(1) if H > 1 else D)
+def _call(dev: int, name: str, *args) -> None:
+    """lib().<name>(*args, the current stream of device `dev`) with that device current; raises on an error status."""
+    f = getattr(lib(), name)
+    if dev == _current_device():
+        st = f(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _raw_stream(dev))
+    if st:
+        raise FP8QError(st, name)
 
 
-def _require_list(t: torch.Tensor, name: str, dtype, numel: int, dev: int) -> None:
-    """A 1-D operand: contiguous, of exactly numel elements, on CUDA device `dev`."""
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{dev}" if dev >= 0 else ""))
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != numel or not t.is_contiguous():
+def _where(dev: int) -> str:
+    return f" on cuda:{dev}" if dev >= 0 else ""
+
+
+def _heads(t: torch.Tensor, name: str, dev: int, shape) -> Tuple[int, int]:
+    """(token, head) strides of a bf16 tensor of `shape` [tokens, heads, head_dim] with contiguous elements on CUDA
+    device `dev`; those of dimensions of size 1 as in a contiguous tensor."""
+    if t.get_device() != dev or dev < 0 or t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor{_where(dev)}, got {t.dtype} on {t.device}")
+    if len(shape) != 3 or t.shape != shape:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] = {tuple(shape)}, got {tuple(t.shape)}")
+    T, H, D = shape
+    a, b, c = t.stride()
+    if c != 1 and D != 1:
+        raise ValueError(f"{name} must have unit stride in the last dimension")
+    return (a if T > 1 else H * D), (b if H > 1 else D)
+
+
+def _list(t: torch.Tensor, name: str, dtype, numel: int, dev: int) -> int:
+    """The address of a 1-D operand: contiguous, of exactly numel elements, on CUDA device `dev`."""
+    if t.get_device() != dev or dev < 0 or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor{_where(dev)}, got {t.dtype} on {t.device}")
+    if t.dim() != 1 or t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {numel} elements")
+    return t.data_ptr()
 
 
 def fp8q_rope_frequencies(rot_dim: int, theta: float = 500000.0, scaling: Optional[dict] = None,
@@ -468,20 +473,15 @@ def fp8q_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, inte
               inverse: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotate bf16 heads x [T, H, D] by positions [T] (int64) times freq (fp64 [rot_dim / 2], from
     fp8q_rope_frequencies); elements from rot_dim on are copied.  `out` may be x itself."""
-    dev = x.get_device()
-    _require_heads(x, "x", dev)
-    shape = x.shape
+    dev, shape = x.get_device(), x.shape
+    xt, xh = _heads(x, "x", dev, shape)
     T, H, D = shape
-    _require_list(positions, "positions", torch.int64, T, dev)
     pairs = freq.numel()
-    _require_list(freq, "freq", torch.float64, pairs, dev)
+    at, f = _list(positions, "positions", torch.int64, T, dev), _list(freq, "freq", torch.float64, pairs, dev)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    elif out is not x:
-        _require_heads(out, "out", dev, shape)
-    xt, xh = _head_strides(x, T, H, D)
-    yt, yh = _head_strides(out, T, H, D)
-    _call(dev, "fp8q_rope", x.data_ptr(), T, H, D, xt, xh, positions.data_ptr(), freq.data_ptr(), 2 * pairs,
+    yt, yh = (xt, xh) if out is x else _heads(out, "out", dev, shape)
+    _call(dev, "fp8q_rope", x.data_ptr(), T, H, D, xt, xh, at, f, 2 * pairs,
           (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), mscale, out.data_ptr(), yt, yh)
     return out
 
@@ -532,37 +532,28 @@ def fp8q_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: to
     dev = cache._dev
     T = k.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
-    _require_heads(k, "k", dev, shape)
-    _require_heads(v, "v", dev, shape)
-    _require_list(slots, "slots", torch.int64, T, dev)
-    R, pos, f = 0, None, None
+    kt, kh = _heads(k, "k", dev, shape)
+    vt, vh = _heads(v, "v", dev, shape)
+    R, at, f = 0, None, None
     if positions is not None and freq is not None:
-        _require_list(positions, "positions", torch.int64, T, dev)
-        R = 2 * freq.numel()
-        _require_list(freq, "freq", torch.float64, R // 2, dev)
-        pos, f = positions.data_ptr(), freq.data_ptr()
+        pairs = freq.numel()
+        R = 2 * pairs
+        at, f = _list(positions, "positions", torch.int64, T, dev), _list(freq, "freq", torch.float64, pairs, dev)
     elif positions is not None or freq is not None:
         raise ValueError("positions and freq are given together")
-    kt, kh = _head_strides(k, *shape)
-    vt, vh = _head_strides(v, *shape)
-    _call(dev, "fp8q_kv4_append", cache._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), T, pos, f, R,
-          ROPE_INTERLEAVED if interleaved else 0, mscale)
+    _call(dev, "fp8q_kv4_append", cache._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+          _list(slots, "slots", torch.int64, T, dev), T, at, f, R, ROPE_INTERLEAVED if interleaved else 0, mscale)
 
 
 def fp8q_kv4_read(cache: KV4Cache, slots: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
     """The cached keys and values of slots [T] (int64) as bf16 [T, kv_heads, head_dim]; zeros for a negative slot."""
     dev, T = cache._dev, slots.numel()
-    _require_list(slots, "slots", torch.int64, T, dev)
+    at = _list(slots, "slots", torch.int64, T, dev)
     shape = (T, cache.kv_heads, cache.head_dim)
-    if out is None:
-        k, v = torch.empty((2, *shape), dtype=torch.bfloat16, device=cache.device)
-    else:
-        k, v = out
-        _require_heads(k, "k", dev, shape)
-        _require_heads(v, "v", dev, shape)
-    kt, kh = _head_strides(k, *shape)
-    vt, vh = _head_strides(v, *shape)
-    _call(dev, "fp8q_kv4_read", cache._ref, slots.data_ptr(), T, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh)
+    k, v = torch.empty((2, *shape), dtype=torch.bfloat16, device=cache.device) if out is None else out
+    kt, kh = _heads(k, "k", dev, shape)
+    vt, vh = _heads(v, "v", dev, shape)
+    _call(dev, "fp8q_kv4_read", cache._ref, at, T, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh)
     return k, v
 
 
@@ -583,39 +574,35 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tenso
     (None: one row per sequence).  Rows behind q_start[B] are left as they were.  lse: fp32 [T, q_heads], written
     when given.  `workspace`: a zero-filled uint8 buffer of fp8q_kv4_attention_workspace_size bytes (allocated here
     when None; left zero).  -> out bf16 [T, q_heads, head_dim]"""
-    dev = cache._dev
-    _require_heads(q, "q", dev)
-    shape = q.shape
+    dev, shape = cache._dev, q.shape
+    qt, qh = _heads(q, "q", dev, shape)
     T, Hq, D = shape
     if D != cache.head_dim:
         raise ValueError(f"q must have head_dim {cache.head_dim}")
-    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.get_device() != dev or \
-            (page_table.stride(1) != 1 and page_table.shape[1] > 1):
-        raise ValueError("page_table must be int32 [sequences, max_pages] on the cache's device, rows contiguous")
-    B, max_pages = page_table.shape
-    _require_list(kv_len, "kv_len", torch.int32, B, dev)
-    if q_start is not None:
-        _require_list(q_start, "q_start", torch.int32, B + 1, dev)
+    if page_table.dtype is not torch.int32 or page_table.get_device() != dev or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [sequences, max_pages] on the cache's device")
+    (B, max_pages), (row, unit) = page_table.shape, page_table.stride()
+    if unit != 1 and max_pages > 1:
+        raise ValueError("page_table's rows must be contiguous")
+    lens = _list(kv_len, "kv_len", torch.int32, B, dev)
+    starts = None if q_start is None else _list(q_start, "q_start", torch.int32, B + 1, dev)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _require_heads(out, "out", dev, shape)
-    if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or
-                            not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous fp32 {(T, Hq)} on the cache's device")
+    ot, oh = _heads(out, "out", dev, shape)
+    sums = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous fp32 {(T, Hq)} on the cache's device")
+        sums = lse.data_ptr()
     if workspace is None:
         workspace = torch.zeros(fp8q_kv4_attention_workspace_size(cache, B, T, Hq, max_q_len), dtype=torch.uint8,
                                 device=q.device)
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
-    qt, qh = _head_strides(q, T, Hq, D)
-    ot, oh = _head_strides(out, T, Hq, D)
     _call(dev, "fp8q_kv4_attention", cache._ref, q.data_ptr(), qt, qh, T, Hq, page_table.data_ptr(),
-          page_table.stride(0) if B > 1 else max_pages, max_pages, kv_len.data_ptr(),
-          None if q_start is None else q_start.data_ptr(), B, max_q_len, D ** -0.5 if sm_scale is None else sm_scale,
-          1 if causal else 0, window, out.data_ptr(), ot, oh, None if lse is None else lse.data_ptr(),
-          workspace.data_ptr(), workspace.numel())     # its size is checked by the library (FP8Q_ERR_INVALID_ARG)
-    return out
+          row if B > 1 else max_pages, max_pages, lens, starts, B, max_q_len, D ** -0.5 if sm_scale is None else sm_scale,
+          1 if causal else 0, window, out.data_ptr(), ot, oh, sums, workspace.data_ptr(), workspace.numel())
+    return out                     # (the workspace's size is checked by the library: FP8Q_ERR_INVALID_ARG)
 
 
 def device_error(clear: bool = True) -> int:

@@ -233,13 +233,16 @@ class S(T):
     def get_device(self):
         return self.device.index if self.is_cuda else -1
 
+    def stride(self, i=None):
+        return self._strides if i is None else self._strides[i]
+
 
 @pytest.fixture
 def lib(monkeypatch):
     rec = Lib()
     monkeypatch.setattr(fq, "lib", lambda: rec)
     monkeypatch.setattr(fq, "_raw_stream", lambda dev: 0)
-    monkeypatch.setattr(fq.torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(fq, "_current_device", lambda: 0)
     return rec
 
 
