@@ -88,7 +88,10 @@ struct AttentionPlan {
 AttentionPlan attention_plan(const fp8q_kv4_cache* c, int64_t T, int64_t Hq, int64_t max_q_len, int sms) {
   const int64_t rows = (max_q_len < T ? max_q_len : T) * (Hq / c->kv_heads);
   AttentionPlan a;
-  a.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 32 ? 4 : 0));
+  // Rows of a key head (the group's heads times the new tokens).  Two tiles of 32 rows in the kernel for few rows still
+  // beat a tensor-memory tile that is half empty (16 sequences of 3000 keys, D = 128: 64 rows 81 us against 89, of 500
+  // keys 22 against 39); three do not (96 rows: 108 against 89).
+  a.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 64 ? 4 : 0));
   a.ctas = sms * (a.nt == 1 ? (c->head_dim == 64 ? 5 : 4) : (a.nt == 2 ? 3 : (a.nt == 4 ? 2 : 1)));
   const int most = fp8q::kv4::kMaxCtas;              // of whose counters each CTA has two
   if (a.ctas > most) a.ctas = most;
