@@ -17,6 +17,7 @@ activations, the FP8-Block scheme).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Tuple
 
@@ -37,6 +38,7 @@ ERR_DEVICE_TIMEOUT = 5
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8q.so")
+BINDING_PATH = os.path.join(_HERE, "_kv4_binding.so")
 
 _lib = None
 
@@ -397,6 +399,27 @@ class _CacheStruct(ctypes.Structure):
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
+class _Binding:
+    """csrc/binding.cpp, loaded at the first use: its functions check their operands as the functions below do, call
+    the entry point and return its status, or return None where an operand is not as expected (the function below then
+    says what is wrong, or takes care of a device that is not the current one)."""
+
+    def __getattr__(self, name):
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"_kv4_binding.so not built ({BINDING_PATH}); run "
+                              "python -m fp8_w8a8_quantized_amax_b200.build")
+        spec = importlib.util.spec_from_file_location("_kv4_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        for f in ("rope", "append", "read", "attention"):
+            setattr(self, f, getattr(module, f))
+        return getattr(module, name)
+
+
+_binding = _Binding()
+
+
 def _raw_stream(dev: int) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
@@ -473,16 +496,19 @@ def fp8q_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, inte
               inverse: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotate bf16 heads x [T, H, D] by positions [T] (int64) times freq (fp64 [rot_dim / 2], from
     fp8q_rope_frequencies); elements from rot_dim on are copied.  `out` may be x itself."""
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    if _binding.rope(x, positions, freq, flags, float(mscale), out) == OK:
+        return out
     dev, shape = x.get_device(), x.shape
     xt, xh = _heads(x, "x", dev, shape)
     T, H, D = shape
     pairs = freq.numel()
     at, f = _list(positions, "positions", torch.int64, T, dev), _list(freq, "freq", torch.float64, pairs, dev)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
     yt, yh = (xt, xh) if out is x else _heads(out, "out", dev, shape)
-    _call(dev, "fp8q_rope", x.data_ptr(), T, H, D, xt, xh, at, f, 2 * pairs,
-          (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), mscale, out.data_ptr(), yt, yh)
+    _call(dev, "fp8q_rope", x.data_ptr(), T, H, D, xt, xh, at, f, 2 * pairs, flags, mscale, out.data_ptr(),
+          yt, yh)
     return out
 
 
@@ -513,7 +539,7 @@ class KV4Cache:
         self.device, self._dev = k_pages.device, k_pages.get_device()
         self._struct = _CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), self.num_pages, self.page_size,
                                     self.kv_heads, self.head_dim, self.k_scale, self.v_scale)
-        self._ref = ctypes.byref(self._struct)
+        self._ref, self._at = ctypes.byref(self._struct), ctypes.addressof(self._struct)
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int = 64, head_dim: int = 128, k_scale: float = 1.0,
@@ -529,7 +555,9 @@ def fp8q_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: to
                     interleaved: bool = False, mscale: float = 1.0) -> None:
     """Quantize k and v (bf16 [T, kv_heads, head_dim]) into the cache's slots ([T] int64, page * page_size + row;
     negative: skipped), k rotated by positions * freq on the way (as it is with both None)."""
-    dev = cache._dev
+    dev, flags = cache._dev, ROPE_INTERLEAVED if interleaved else 0
+    if _binding.append(cache._at, dev, k, v, slots, positions, freq, flags, float(mscale)) == OK:
+        return
     T = k.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
     kt, kh = _heads(k, "k", dev, shape)
@@ -542,15 +570,17 @@ def fp8q_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: to
     elif positions is not None or freq is not None:
         raise ValueError("positions and freq are given together")
     _call(dev, "fp8q_kv4_append", cache._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-          _list(slots, "slots", torch.int64, T, dev), T, at, f, R, ROPE_INTERLEAVED if interleaved else 0, mscale)
+          _list(slots, "slots", torch.int64, T, dev), T, at, f, R, flags, mscale)
 
 
 def fp8q_kv4_read(cache: KV4Cache, slots: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
     """The cached keys and values of slots [T] (int64) as bf16 [T, kv_heads, head_dim]; zeros for a negative slot."""
     dev, T = cache._dev, slots.numel()
-    at = _list(slots, "slots", torch.int64, T, dev)
     shape = (T, cache.kv_heads, cache.head_dim)
     k, v = torch.empty((2, *shape), dtype=torch.bfloat16, device=cache.device) if out is None else out
+    if _binding.read(cache._at, dev, slots, k, v) == OK:
+        return k, v
+    at = _list(slots, "slots", torch.int64, T, dev)
     kt, kh = _heads(k, "k", dev, shape)
     vt, vh = _heads(v, "v", dev, shape)
     _call(dev, "fp8q_kv4_read", cache._ref, at, T, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh)
@@ -575,6 +605,12 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tenso
     when given.  `workspace`: a zero-filled uint8 buffer of fp8q_kv4_attention_workspace_size bytes (allocated here
     when None; left zero).  -> out bf16 [T, q_heads, head_dim]"""
     dev, shape = cache._dev, q.shape
+    if sm_scale is None:
+        sm_scale = cache.head_dim ** -0.5
+    if out is not None and workspace is not None and \
+            _binding.attention(cache._at, dev, q, page_table, kv_len, q_start, max_q_len, float(sm_scale), bool(causal),
+                               window, out, lse, workspace) == OK:
+        return out
     qt, qh = _heads(q, "q", dev, shape)
     T, Hq, D = shape
     if D != cache.head_dim:
@@ -600,7 +636,7 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tenso
     elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
     _call(dev, "fp8q_kv4_attention", cache._ref, q.data_ptr(), qt, qh, T, Hq, page_table.data_ptr(),
-          row if B > 1 else max_pages, max_pages, lens, starts, B, max_q_len, D ** -0.5 if sm_scale is None else sm_scale,
+          row if B > 1 else max_pages, max_pages, lens, starts, B, max_q_len, sm_scale,
           1 if causal else 0, window, out.data_ptr(), ot, oh, sums, workspace.data_ptr(), workspace.numel())
     return out                     # (the workspace's size is checked by the library: FP8Q_ERR_INVALID_ARG)
 

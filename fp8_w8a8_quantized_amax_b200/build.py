@@ -10,6 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8q.so")
+BINDING = os.path.join(HERE, "_kv4_binding.so")
 OBJ = os.path.join(HERE, "_build")
 SOURCES = ["fp8q.cu", "kv4.cu"]
 # What each source file is made of; the public header belongs to both.
@@ -88,8 +89,33 @@ def _compile(out: str, extra: list, force: bool, verbose: bool) -> str:
     return out
 
 
+def build_binding(force: bool = False) -> str:
+    """_kv4_binding.so: the operand checks and calls of the KV-cache entry points in C++ (g++, torch's headers)."""
+    if not force and not _older(BINDING, ["binding.cpp"]):
+        return BINDING
+    import sysconfig
+
+    import torch
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    t = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for path in (os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp", "-L", os.path.join(t, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + r.stdout + r.stderr)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    return _compile(LIB, [], force, verbose)
+    _compile(LIB, [], force, verbose)
+    build_binding(force)
+    return LIB
 
 
 def build_test_hooks(force: bool = False) -> str:

@@ -579,3 +579,49 @@ def test_prompt_then_tokens(H, Hq, D, page, interleaved):
                 n * 2.0 ** -24 * np.abs(v_all[b]).max() + 2.0 ** -8 * np.abs(o)
             assert np.all(np.abs(O.f64(out[r:r + m]) - o) <= tol)
             r += m
+
+
+# ------------------------------------------------------------- the binding ---
+
+def test_cpp_and_python_calls_agree(monkeypatch):
+    """The operands' way through the C++ binding and through ctypes: the same results, the same refusals."""
+    b = Batch([200, 70], [2, 1], 8, 2, 128, 32, seed=11)
+    freq, pos = fq.fp8q_rope_frequencies(128), torch.tensor([5, 6, 9], device=DEV)
+    k, v = heads(3, 2, 128, 1, wide=6, at=2), heads(3, 2, 128, 2)
+    slots = torch.tensor([3, -1, 40], device=DEV)
+    ws = torch.zeros(fq.fp8q_kv4_attention_workspace_size(b.cache, 2, 3, 8, 2), dtype=torch.uint8, device=DEV)
+
+    def everything():
+        cache = new_cache(4, 2, 32, 128, seed=5)
+        fq.fp8q_kv4_append(cache, k, v, slots, pos, freq, interleaved=True, mscale=1.25)
+        out, lse = b.call(workspace=ws, window=33)
+        return [fq.fp8q_rope(b.q, pos, freq, inverse=True), cache.k_pages, cache.v_pages,
+                *fq.fp8q_kv4_read(cache, slots), out, lse]
+
+    def refusals():
+        for call in (lambda: fq.fp8q_rope(b.q.float(), pos, freq), lambda: fq.fp8q_rope(b.q, pos[:2], freq),
+                     lambda: fq.fp8q_rope(b.q, pos, freq.float()), lambda: fq.fp8q_rope(b.q.cpu(), pos, freq),
+                     lambda: fq.fp8q_kv4_append(b.cache, k[:2], v, slots), lambda: fq.fp8q_kv4_append(b.cache, k, v, slots, pos),
+                     lambda: fq.fp8q_kv4_read(b.cache, slots.int()), lambda: b.call(workspace=ws.float()),
+                     lambda: b.call(workspace=ws, q_start=b.q_start[:2]), lambda: b.call(workspace=ws, lse=torch.zeros(3, 8))):
+            with pytest.raises(ValueError):
+                call()
+        for call in (lambda: fq.fp8q_rope(b.q, pos, freq, mscale=0.0), lambda: b.call(workspace=ws, window=-1),
+                     lambda: b.call(workspace=ws[:100]), lambda: b.call(workspace=ws, max_q_len=0),
+                     lambda: fq.fp8q_kv4_append(b.cache, k, v, slots, pos, freq, mscale=float("nan"))):
+            with pytest.raises(fq.FP8QError) as e:
+                call()
+            assert e.value.status == fq.ERR_INVALID_ARG
+
+    fast = everything()
+    refusals()
+
+    class Never:
+        def __getattr__(self, name):
+            return lambda *a: None
+
+    monkeypatch.setattr(fq, "_binding", Never())
+    slow = everything()
+    refusals()
+    for x, y in zip(fast, slow):
+        assert torch.equal(x, y)

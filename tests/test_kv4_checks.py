@@ -361,3 +361,30 @@ def test_the_plain_form_attends():
     assert np.allclose(lse, torch.logsumexp(s, -1).numpy())
     o, lse, _, _ = O.attention(q, k[:, :3], v[:, :3], 0.3)
     assert np.all(o[:2] == 0) and np.all(np.isneginf(lse[:2])) and np.all(np.isfinite(lse[2:]))
+
+
+# ----------------------------------------------------------- the C++ calls ---
+
+def test_cpp_binding_leaves_unexpected_operands_to_python(L):
+    """Whatever is not a CUDA tensor of the expected kind: None, and nothing is called."""
+    b = fq._binding
+    x, i, f = torch.zeros(4, 2, 64, dtype=BF), torch.zeros(4, dtype=I64), torch.zeros(32, dtype=F64)
+    c = cache(head_dim=64, kv_heads=2)
+    at = ctypes.addressof(c)
+    assert b.rope(x, i, f, 0, 1.0, x) is None                     # on the CPU
+    assert b.rope(x, i, f, 0, 1.0) is None                        # too few
+    assert b.rope(None, i, f, 0, 1.0, x) is None
+    assert b.rope(S((4, 2, 64), BF), i, f, 0, 1.0, x) is None     # not a tensor
+    assert b.append(at, 0, x, x, i, None, None, 0, 1.0) is None
+    assert b.append("no address", 0, x, x, i, None, None, 0, 1.0) is None
+    assert b.append(at, 1 << 70, x, x, i, None, None, 0, 1.0) is None
+    assert b.read(at, 0, i, x, x) is None
+    assert b.attention(at, 0, x, i, i, None, 1, 1.0, True, 0, x, None, x) is None
+    sparse = torch.sparse_coo_tensor(torch.zeros(3, 1, dtype=I64), torch.ones(1, dtype=BF), (4, 2, 64))
+    assert b.rope(sparse, i, f, 0, 1.0, x) is None
+
+
+def test_package_fails_loudly_without_the_cpp_binding(monkeypatch, L):
+    monkeypatch.setattr(fq, "BINDING_PATH", "/nonexistent/_kv4_binding.so")
+    with pytest.raises(ImportError):
+        fq._Binding().rope
