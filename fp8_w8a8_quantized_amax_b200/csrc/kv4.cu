@@ -329,7 +329,7 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   if (st != FP8Q_OK) return st;
   if (T < 0 || B < 0 || Hq <= 0 || max_q_len <= 0 || max_pages < 0 || window < 0) return FP8Q_ERR_INVALID_ARG;
   if (Hq % cache->kv_heads != 0 || (causal != 0 && causal != 1)) return FP8Q_ERR_INVALID_ARG;
-  if (!finite_positive(sm_scale)) return FP8Q_ERR_INVALID_ARG;
+  if (!finite_positive(sm_scale) || !(sm_scale * cache->k_scale < 1.0e38f)) return FP8Q_ERR_INVALID_ARG;
   if (T == 0 || B == 0) return FP8Q_OK;
   if (!q_start && (T < B || max_q_len != 1)) return FP8Q_ERR_INVALID_ARG;
   if ((st = check_rows(Q_bf16, q_token_stride, q_head_stride)) != FP8Q_OK) return st;
@@ -341,7 +341,11 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
       !aligned(workspace, 16))
     return FP8Q_ERR_MISALIGNED;
   if (T > kInt32Max || Hq > 65536 || T * Hq > kInt32Max || B > 65536 || table_stride > kStrideMax ||
-      max_pages > kInt32Max || max_pages * cache->page_size > kInt32Max)
+      max_pages > kInt32Max || max_pages * cache->page_size > kInt32Max - 65536)   // (keys past a length are ints too)
+    return FP8Q_ERR_UNSUPPORTED;
+  // the kernels count items in 23 bits and steps in 40
+  const int64_t items = B * cache->kv_heads * attention_plan(cache, T, Hq, max_q_len, 1).row_tiles;
+  if (items >= (1 << 22) || items * (max_pages * cache->page_size / 128 + 8) >= (static_cast<int64_t>(1) << 39))
     return FP8Q_ERR_UNSUPPORTED;
   int dev, sms;
   if ((st = current_device(&dev, &sms)) != FP8Q_OK) return st;
@@ -368,10 +372,6 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   p.causal = causal;
   p.window = window;
   const AttentionPlan plan = attention_plan(cache, T, Hq, max_q_len, sms);
-  // the kernels count items in 23 bits and steps in 40
-  const int64_t items = B * cache->kv_heads * plan.row_tiles;
-  if (items >= (1 << 22) || items * (max_pages * cache->page_size / 128 + 8) >= (static_cast<int64_t>(1) << 39))
-    return FP8Q_ERR_UNSUPPORTED;
   if (workspace_bytes < plan.bytes()) return FP8Q_ERR_INVALID_ARG;
   p.count = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);

@@ -434,10 +434,13 @@ FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* s
  *   sequence (behind q_start[B]) are left as they were.
  *   Q_bf16, O_bf16  [T, Hq, D], 16-byte aligned, strides % 8 == 0; O's rows must
  *                   not overlap.  Q's values must be finite.
- *   page_table      [B, max_pages] int32, row stride table_stride.
+ *   page_table      [B, max_pages] int32, row stride table_stride >= max_pages;
+ *                   max_pages * page_size < 2^31 - 65536.  Entries that no visible
+ *                   key needs are not read.
  *   kv_len          [B] int32, 0 <= kv_len[b] <= max_pages * page_size.
  *   q_start         [B + 1] int32, ascending, q_start[B] <= T; NULL for one row
  *                   per sequence (row b is sequence b's; then max_q_len is 1).
+ *   sm_scale        > 0, finite, as is its product with k_scale (1 / sqrt(D) for most models).
  *   max_q_len       the largest number of rows of a sequence; longer ones set the
  *                   device error word.  Lengths stay on the device: a captured call
  *                   can be replayed with other lengths up to these bounds.
@@ -447,6 +450,8 @@ FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* s
  *                   zero by every completed call, of any sizes; what lies behind them is
  *                   scratch (so it is not to be shared with fp8_linear's workspace).  Not
  *                   shared by concurrent calls.
+ *   After a call that failed on the device (fp8q_device_error nonzero), zero the
+ *   workspace's header again.
  *   A bad length or page index on the device never leads out of the tensors: it
  *   sets the device error word, and the rows concerned are not to be used.
  */

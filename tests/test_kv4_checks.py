@@ -219,7 +219,9 @@ def test_read_arguments(L, kw, want):
     (dict(ws=None), INV), (dict(ws=P + 8), MIS),
     (dict(qs=None), INV),                                      # one row per sequence: max_q_len is 1
     (dict(qs=None, mq=1), VALID), (dict(qs=None, mq=1, T=2), INV),
-    (dict(B=70000, T=70000), UNS), (dict(mp=1 << 30, ts=1 << 30), UNS), (dict(T=1 << 27, Hq=32, ot=4096), UNS),
+    (dict(c=cache(k_scale=1e20), sm=1e20), INV), (dict(c=cache(k_scale=1e-20), sm=1e20), VALID),
+    (dict(B=70000, T=70000), UNS), (dict(mp=1 << 30, ts=1 << 30), UNS), (dict(mp=(1 << 25) - 1, ts=1 << 25), UNS),
+    (dict(mp=1 << 24, ts=1 << 24), VALID), (dict(B=60000, T=60000, mq=5000), UNS), (dict(T=1 << 27, Hq=32, ot=4096), UNS),
 ])
 def test_attention_arguments(L, kw, want):
     assert attend(L, **kw) == want
