@@ -223,7 +223,7 @@ fp8q_status fp8q_rope(const void* X_bf16, int64_t T, int64_t H, int64_t D, int64
   // spread over the SMs by heads instead.
   const int tokens = T >= 16ll * sms ? 4 : 1;
   const int64_t units = H * (rot_dim / 16);
-  int64_t split = T < sms ? (units + 511) / 512 : 1;
+  int64_t split = T < sms ? (units + 255) / 256 : 1;
   if (split > H) split = H;
   const dim3 grid(static_cast<unsigned>((T + tokens - 1) / tokens), static_cast<unsigned>(split));
   const size_t bytes = static_cast<size_t>(tokens) * (rot_dim / 2) * sizeof(float2);
@@ -307,7 +307,7 @@ fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* slots, int
   p.T = static_cast<int>(T);
   const int64_t items = 2 * T * cache->kv_heads * (cache->head_dim / 16);
   auto k = cache->head_dim == 64 ? fp8q::kv4::read_kernel<64> : fp8q::kv4::read_kernel<128>;
-  return launch(k, dim3(blocks_for(items, 512, kInt32Max)), dim3(256), 0, stream, p);
+  return launch(k, dim3(blocks_for(items, 256, kInt32Max)), dim3(256), 0, stream, p);
 }
 
 size_t fp8q_kv4_attention_workspace_size(const fp8q_kv4_cache* cache, int64_t B, int64_t T, int64_t Hq,

@@ -241,60 +241,43 @@ struct ReadParams {
 };
 
 // The cached values of the given slots as bf16 (zeros for a negative slot): one
-// thread per 16 elements, two in flight.
+// thread per 16 elements of one row, as many threads as there are such blocks.
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int kBlocks = D / 16, kFlight = 2;
+  constexpr int kBlocks = D / 16;
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t heads = static_cast<uint32_t>(p.c.heads), per_token = 2 * heads;
-  const uint32_t rows = static_cast<uint32_t>(p.T) * per_token;          // (token, K or V, head)
+  const uint32_t row = blockIdx.x * (256 / kBlocks) + threadIdx.x / kBlocks;   // (token, K or V, head)
+  if (row >= static_cast<uint32_t>(p.T) * per_token) return;
   const int block = threadIdx.x % kBlocks;
-  const uint32_t step = gridDim.x * (256 / kBlocks);
-  for (uint32_t r = blockIdx.x * (256 / kBlocks) + threadIdx.x / kBlocks; r < rows; r += kFlight * step) {
-    uint2 codes[kFlight];
-    uint32_t scale[kFlight];
-    uint16_t* y[kFlight];
-    float g[kFlight];
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const uint32_t row = r + i * step;
-      y[i] = nullptr;
-      if (row >= rows || row < r) continue;          // (past the end, or past 2^32)
-      const uint32_t t = row / per_token, rest = row - t * per_token;
-      const bool is_v = rest >= heads;
-      const uint32_t h = is_v ? rest - heads : rest;
-      int64_t slot = p.slots[t];
-      if (slot >= p.c.pages * p.c.page_size) {
-        atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadSlot));
-        slot = -1;
-      }
-      y[i] = (is_v ? p.v + t * p.vt + h * p.vh : p.k + t * p.kt + h * p.kh) + block * 16;
-      g[i] = is_v ? p.c.vg : p.c.kg;
-      codes[i] = make_uint2(0, 0);
-      scale[i] = 0;
-      if (slot >= 0) {
-        const uint8_t* base = is_v ? p.c.v : p.c.k;
-        const int64_t page = slot >> p.c.page_shift;
-        const int in_page = static_cast<int>(slot) & (p.c.page_size - 1);
-        codes[i] = *reinterpret_cast<const uint2*>(base + p.c.code_offset(page, h, in_page) + block * 8);
-        scale[i] = base[p.c.scale_offset(page, h, in_page) + block];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      if (y[i] == nullptr) continue;
-      const float s = f16lo(widen_e4m3x2(scale[i]));
-      uint32_t o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {                  // code * scale is exact; then one fp32 product, one rounding to bf16
-        const uint32_t w = widen_e2m1x2((j < 4 ? codes[i].x : codes[i].y) >> (8 * (j & 3)));
-        o[j] = pack_bf16x2(f16lo(w) * s * g[i], f16hi(w) * s * g[i]);
-      }
-      reinterpret_cast<uint4*>(y[i])[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<uint4*>(y[i])[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
+  const uint32_t t = row / per_token, rest = row - t * per_token;
+  const bool is_v = rest >= heads;
+  const uint32_t h = is_v ? rest - heads : rest;
+  int64_t slot = p.slots[t];
+  if (slot >= p.c.pages * p.c.page_size) {
+    atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadSlot));
+    slot = -1;
   }
+  uint2 codes = make_uint2(0, 0);
+  uint32_t scale = 0;
+  if (slot >= 0) {
+    const uint8_t* base = is_v ? p.c.v : p.c.k;
+    const int64_t page = slot >> p.c.page_shift;
+    const int in_page = static_cast<int>(slot) & (p.c.page_size - 1);
+    codes = *reinterpret_cast<const uint2*>(base + p.c.code_offset(page, h, in_page) + block * 8);
+    scale = base[p.c.scale_offset(page, h, in_page) + block];
+  }
+  const float s = f16lo(widen_e4m3x2(scale)), g = is_v ? p.c.vg : p.c.kg;
+  uint32_t o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {                      // code * scale is exact; then one fp32 product, one rounding to bf16
+    const uint32_t w = widen_e2m1x2((j < 4 ? codes.x : codes.y) >> (8 * (j & 3)));
+    o[j] = pack_bf16x2(f16lo(w) * s * g, f16hi(w) * s * g);
+  }
+  uint4* y = reinterpret_cast<uint4*>((is_v ? p.v + t * p.vt + h * p.vh : p.k + t * p.kt + h * p.kh) + block * 16);
+  y[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  y[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 }  // namespace kv4
