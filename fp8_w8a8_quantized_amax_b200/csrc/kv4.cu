@@ -88,11 +88,13 @@ struct AttentionPlan {
 AttentionPlan attention_plan(const fp8q_kv4_cache* c, int64_t T, int64_t Hq, int64_t max_q_len, int sms) {
   const int64_t rows = (max_q_len < T ? max_q_len : T) * (Hq / c->kv_heads);
   AttentionPlan a;
-  // Rows of a key head (the group's heads times the new tokens).  Two tiles of 32 rows in the kernel for few rows still
-  // beat a tensor-memory tile that is half empty (16 sequences of 3000 keys, D = 128: 64 rows 81 us against 89, of 500
-  // keys 22 against 39); three do not (96 rows: 108 against 89).
-  a.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 64 ? 4 : 0));
-  a.ctas = sms * (a.nt == 1 ? (c->head_dim == 64 ? 5 : 4) : (a.nt == 2 ? 3 : (a.nt == 4 ? 2 : 1)));
+  // Rows of a key head (the group's heads times the new tokens), D = 128.  Tiles of 8 have four CTAs an SM and little
+  // to join, tiles of 16 dequantize a key for twice the rows.  24 rows: three tiles of 8 against two of 16 take 37
+  // against 38 us for 16 sequences of 4096 keys, 17 against 20 for ones of 700, 78 against 75 for 32 of 8000; 32 rows:
+  // 47 against 47, 19 against 22, 104 against 95.  Half a tensor-memory tile pays from six tiles of 16 on: 80 rows 84
+  // against 88, 31 against 44, 200 against 194 us; 96 rows: 96 against 88, 34 against 44, 239 against 193.
+  a.nt = rows <= 24 ? 1 : (rows <= 80 ? 2 : 0);
+  a.ctas = sms * (a.nt == 1 ? (c->head_dim == 64 ? 5 : 4) : (a.nt == 2 ? 3 : 1));
   const int most = fp8q::kv4::kMaxCtas;              // of whose counters each CTA has two
   if (a.ctas > most) a.ctas = most;
   const int64_t tile = a.nt ? 8 * a.nt : fp8q::kv4::many::kRows;
@@ -376,16 +378,20 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   p.count = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
   p.row_tiles = plan.row_tiles;
+  // No more CTAs than there can be steps of 128 keys: CTAs without work are not free, and where they fill the SMs the
+  // few that have some come to share an SM (64 rows of 8 heads over 500 keys: 16 -> 12 us).
+  int64_t keys = max_pages * cache->page_size;
+  if (window > 0 && keys > window + p.max_q + 128) keys = window + p.max_q + 128;
+  const int64_t steps = items * ((keys + 127) / 128 + 1);
+  const int ctas = static_cast<int>(plan.ctas < steps ? plan.ctas : steps);
   if (cache->head_dim == 128) {
-    if (plan.nt == 1) return launch_few<128, 1, 4>(p, plan.ctas, dev, stream);
-    if (plan.nt == 2) return launch_few<128, 2, 3>(p, plan.ctas, dev, stream);
-    if (plan.nt == 4) return launch_few<128, 4, 2>(p, plan.ctas, dev, stream);
-    return launch_many<128>(p, plan.ctas, dev, stream);
+    if (plan.nt == 1) return launch_few<128, 1, 4>(p, ctas, dev, stream);
+    if (plan.nt == 2) return launch_few<128, 2, 3>(p, ctas, dev, stream);
+    return launch_many<128>(p, ctas, dev, stream);
   }
-  if (plan.nt == 1) return launch_few<64, 1, 5>(p, plan.ctas, dev, stream);
-  if (plan.nt == 2) return launch_few<64, 2, 3>(p, plan.ctas, dev, stream);
-  if (plan.nt == 4) return launch_few<64, 4, 2>(p, plan.ctas, dev, stream);
-  return launch_many<64>(p, plan.ctas, dev, stream);
+  if (plan.nt == 1) return launch_few<64, 1, 5>(p, ctas, dev, stream);
+  if (plan.nt == 2) return launch_few<64, 2, 3>(p, ctas, dev, stream);
+  return launch_many<64>(p, ctas, dev, stream);
 }
 
 }  // extern "C"

@@ -75,6 +75,9 @@ struct Range {
   }
 };
 
+// A sum over the list holds its steps in the low 40 bits and its items above (the host bounds both).
+constexpr int64_t kOneItem = static_cast<int64_t>(1) << 40;
+
 // The softmax base is raised only when a score passes it by 2^kSlack: P, at most 256, keeps its precision in f16.
 constexpr float kSlack = 8.0f;
 
@@ -180,11 +183,6 @@ constexpr int kJoin = 16;     // parts of an item joined at a time
 constexpr int kOver = 3;
 constexpr int kJoinCost = 4;  // steps that joining an item's parts takes
 
-// Q fragments in shared memory instead of 16 NT registers: at 32 rows, and at 8, where the loop then has no spills with
-// four CTAs an SM (five at D = 64; five at D = 128 spilled: 77 us against 70 us for 32 sequences of 8192 keys).
-template <int NT>
-constexpr bool kQInSmem = NT != 2;
-
 template <int D, int NT, int WARPS>
 struct Layout {
   static constexpr int kThreads = 32 * WARPS;
@@ -193,17 +191,16 @@ struct Layout {
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
   static constexpr int kStageBytes = 2 * (kCodes + kScales);       // K codes, K scales, V codes, V scales
   static constexpr int kRedStride = D + 4;
-  // [kRows][kRedStride] fp32 a warp: over the warp's free stage where it fits (it does at NT = 1), else apart
-  static constexpr bool kRedInStage = kRows * kRedStride * 4 <= kStageBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kRed = WARPS * kWarpBytes;
-  static constexpr int kMl = kRed + (kRedInStage ? 0 : WARPS * kRows * kRedStride * 4);   // [WARPS][kRows] m, then l
-  static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // Q fragments, where they are kept in shared memory
-  // the rows of the current and the next job's queries as they are (bf16), where there is room: at NT = 1
-  static constexpr int kRaw = kQ + (kQInSmem<NT> ? NT * (D / 16) * 32 * 8 : 0);
-  static constexpr bool kQAhead = NT == 1;
+  // [8][kRedStride] fp32 a warp, over the warp's free stage: the partial results meet eight rows at a time
+  static_assert(8 * kRedStride * 4 <= kStageBytes, "eight rows in a stage");
+  // and the bases and sums of as many parts as are joined at a time (kJoin, or the groups of kJoin that there can be)
+  static_assert(kMaxCtas / kJoin >= kJoin && kMaxCtas / kJoin / WARPS * kRows * 8 <= kStageBytes, "over the free stages");
+  static constexpr int kMl = WARPS * kWarpBytes;                   // [WARPS][kRows] m, then l
+  static constexpr int kQ = kMl + 2 * WARPS * kRows * 4;           // Q fragments
+  static constexpr int kRaw = kQ + NT * (D / 16) * 32 * 8;         // the current and the next job's query rows, as they are
   static constexpr int kRawBytes = kRows * D * 2;
-  static constexpr int kMisc = kRaw + (kQAhead ? 2 * kRawBytes : 0);
+  static constexpr int kMisc = kRaw + 2 * kRawBytes;
   static constexpr int kJobs = kMisc + 128;                        // two jobs of at most 64 bytes
   static constexpr int kBytes = kJobs + 128;
   static constexpr int kPart = kRows * (D + 2);                    // floats of a partial result
@@ -230,8 +227,6 @@ __device__ __forceinline__ Span span(const AttnParams& p, int b) {
 
 // A CTA's part of one item: `steps` steps from step `step`, key `key` on, its
 // place in the list, and what the item is.
-constexpr int64_t kOneItem = static_cast<int64_t>(1) << 40;
-
 struct Job {
   Span x;
   int b, item, step, steps, key;
@@ -267,14 +262,12 @@ template <int D, int NT, int WARPS, int CTAS>
 __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __grid_constant__ AttnParams p) {
   using L = Layout<D, NT, WARPS>;
   constexpr int kRows = L::kRows, kStep = L::kStep, kSteps = D / 16;
-  constexpr int kHalves = NT == 4 ? 1 : 2;          // 16-key halves of a tile worked on together (registers)
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = lane_id(), warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   // warp w's partial O^T at the end of a job; `stage` is then the stage of the next tile, in flight, and the other free
   auto red_of = [&](int w, int stage) {
-    return reinterpret_cast<float*>(L::kRedInStage ? smem + w * L::kWarpBytes + (stage ^ 1) * L::kStageBytes
-                                                   : smem + L::kRed + w * kRows * L::kRedStride * 4);
+    return reinterpret_cast<float*>(smem + w * L::kWarpBytes + (stage ^ 1) * L::kStageBytes);
   };
   float* ml = reinterpret_cast<float*>(smem + L::kMl);
   uint2* qs = reinterpret_cast<uint2*>(smem + L::kQ);
@@ -404,7 +397,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
                       ((key + scale_key) & in_page) * (D / 16));
   };
 
-  uint32_t qf[kQInSmem<NT> ? 1 : NT][kSteps][2];
   // per row: the scores' factor, the base m (negated; 0 before the first key), the score at which it is raised, the sum
   float qscale[NT][2], nbase[NT][2], limit[NT][2], l[NT][2];
   float o[kSteps][NT][4];
@@ -422,16 +414,14 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
   };
   // A job's query rows, on their way while the job before it is worked on (one group of copies).
   auto fetch_rows = [&](int slot) {
-    if constexpr (L::kQAhead) {
-      const Job& j = jobs[slot];
-      const int row0 = j.item / p.c.heads * kRows, rows = min(kRows, j.x.s.n * p.group - row0), head = j.item % p.c.heads;
-      for (int i = threadIdx.x; i < rows * (D / 8); i += L::kThreads) {
-        const int r = i / (D / 8), row = row0 + r;
-        cp_async_16(smem + L::kRaw + slot * L::kRawBytes + i * 16,
-                    p.q + (j.x.s.r0 + row / p.group) * p.qt + (head * p.group + row % p.group) * p.qh + i % (D / 8) * 8);
-      }
-      cp_async_commit();
+    const Job& j = jobs[slot];
+    const int row0 = j.item / p.c.heads * kRows, rows = min(kRows, j.x.s.n * p.group - row0), head = j.item % p.c.heads;
+    for (int i = threadIdx.x; i < rows * (D / 8); i += L::kThreads) {
+      const int r = i / (D / 8), row = row0 + r;
+      cp_async_16(smem + L::kRaw + slot * L::kRawBytes + i * 16,
+                  p.q + (j.x.s.r0 + row / p.group) * p.qt + (head * p.group + row % p.group) * p.qh + i % (D / 8) * 8);
     }
+    cp_async_commit();
   };
   int stage = 0, which = 0;
   fetch_rows(0);
@@ -442,10 +432,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       issue(codes_of(head), scales_of(head), first_pages(0), key, 0);
     cp_async_commit();
   }
-  if constexpr (L::kQAhead) {
-    cp_async_wait<1>();
-    __syncthreads();
-  }
+  cp_async_wait<1>();
+  __syncthreads();
 
   for (;; which ^= 1) {
     // ---- an item (or this CTA's part of it): its query rows, and the next job ----
@@ -471,11 +459,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       const int r = nt * 8 + g;
       uint32_t w[D / 8];
       if (r < rows) {
-        const uint16_t* src;
-        if constexpr (L::kQAhead)
-          src = reinterpret_cast<const uint16_t*>(smem + L::kRaw + which * L::kRawBytes) + r * D + t * (D / 4);
-        else
-          src = p.q + (seq.r0 + (row0 + r) / p.group) * p.qt + (head * p.group + (row0 + r) % p.group) * p.qh + t * (D / 4);
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(smem + L::kRaw + which * L::kRawBytes) + r * D + t * (D / 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -499,12 +483,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       for (int i = 0; i < kSteps; ++i) {
         const uint32_t b0 = pack_f16x2(bf16lo(w[2 * i]) * up, bf16hi(w[2 * i]) * up);
         const uint32_t b1 = pack_f16x2(bf16lo(w[2 * i + 1]) * up, bf16hi(w[2 * i + 1]) * up);
-        if constexpr (kQInSmem<NT>) {
-          if (warp == nt % WARPS) qs[(nt * kSteps + i) * 32 + lane] = make_uint2(b0, b1);
-        } else {
-          qf[nt][i][0] = b0;
-          qf[nt][i][1] = b1;
-        }
+        if (warp == nt % WARPS) qs[(nt * kSteps + i) * 32 + lane] = make_uint2(b0, b1);
       }
       qscale[nt][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
       qscale[nt][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
@@ -558,12 +537,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       // Row r of a 16-key tile is key r ^ (r / 4 & 1): K's rows of neighbouring lane groups and V's rows 2t (and
       // 2t + 1) of the four t then lie in different banks (V: at most two lanes to a bank).
       const int kg = g ^ ((g >> 2) & 1);
+      float sc[2][NT][4];
 #pragma unroll
-      for (int m0 = 0; m0 < 2; m0 += kHalves) {
-      float sc[kHalves][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < kHalves; ++mt) {
-        const int r0 = (m0 + mt) * 16 + kg, r1 = r0 + 8;
+      for (int mt = 0; mt < 2; ++mt) {
+        const int r0 = mt * 16 + kg, r1 = r0 + 8;
         uint32_t w0[D / 32], w1[D / 32], s0[2], s1[2];
         if constexpr (D == 128) {
           const uint4 a = *reinterpret_cast<const uint4*>(kc + r0 * 64 + t * 16);
@@ -597,17 +574,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              uint32_t b0, b1;
-              if constexpr (kQInSmem<NT>) {
-                const uint2 v = qs[(nt * kSteps + 2 * w + h) * 32 + lane];
-                b0 = v.x;
-                b1 = v.y;
-              } else {
-                b0 = qf[nt][2 * w + h][0];
-                b1 = qf[nt][2 * w + h][1];
-              }
-              if (w == 0 && h == 0) mma16816_first(sc[mt][nt], a[0], b[0], a[1], b[1], b0, b1);
-              else mma16816(sc[mt][nt], a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1], b0, b1);
+              const uint2 q = qs[(nt * kSteps + 2 * w + h) * 32 + lane];
+              if (w == 0 && h == 0) mma16816_first(sc[mt][nt], a[0], b[0], a[1], b[1], q.x, q.y);
+              else mma16816(sc[mt][nt], a[2 * h], b[2 * h], a[2 * h + 1], b[2 * h + 1], q.x, q.y);
             }
         }
       }
@@ -623,22 +592,21 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
             const int pos = seq.kv - seq.n + min(row0 + nt * 8 + 2 * t + q, end_row) / p.group;
             const int first = visible_first(p, pos), last = visible_last(p, seq, pos);
 #pragma unroll
-            for (int mt = 0; mt < kHalves; ++mt)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int k = key + (m0 + mt) * 16 + kg + h * 8;
+                const int k = key + mt * 16 + kg + h * 8;
                 if (k < first || k >= last) sc[mt][nt][2 * h + q] = -INFINITY;
               }
           }
       }
-      uint32_t pf[kHalves][NT][2];
+      uint32_t pf[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float top[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          top[i] = fmaxf(sc[0][nt][i], sc[0][nt][i + 2]);
-          if constexpr (kHalves == 2) top[i] = fmaxf(top[i], fmaxf(sc[1][nt][i], sc[1][nt][i + 2]));
+          top[i] = fmaxf(fmaxf(sc[0][nt][i], sc[0][nt][i + 2]), fmaxf(sc[1][nt][i], sc[1][nt][i + 2]));
         }
         if (__any_sync(0xFFFFFFFFu, top[0] > limit[nt][0] || top[1] > limit[nt][1])) {
 #pragma unroll
@@ -663,7 +631,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
         const uint64_t scale2 = f32x2_pack(qscale[nt][0], qscale[nt][1]), base2 = f32x2_pack(nbase[nt][0], nbase[nt][1]);
         uint64_t l2 = f32x2_pack(l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int mt = 0; mt < kHalves; ++mt)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float x, y;
@@ -677,8 +645,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       }
       // V^T: row g (and g + 8) of m-tile i is element g D/8 + 2i (and + 1); columns 2t, 2t + 1 (and + 8) are keys
 #pragma unroll
-      for (int mt = 0; mt < kHalves; ++mt) {
-        const int ka = (m0 + mt) * 16 + (2 * t ^ (t >> 1)), kb = (m0 + mt) * 16 + ((2 * t + 1) ^ (t >> 1));
+      for (int mt = 0; mt < 2; ++mt) {
+        const int ka = mt * 16 + (2 * t ^ (t >> 1)), kb = mt * 16 + ((2 * t + 1) ^ (t >> 1));
         const int keys[4] = {ka, kb, ka + 8, kb + 8};
         uint32_t vw[4][D / 64], sv[4];
 #pragma unroll
@@ -719,7 +687,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
           }
         }
       }
-      }
       __syncwarp();                                 // every lane has read the stage before it is filled again
     }
 
@@ -736,23 +703,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
           ml[(WARPS + warp) * kRows + r] = l[nt][i];
         }
       }
-    __syncthreads();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = nt * 8 + 2 * t + i;
-        float top = -INFINITY;
-        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
-        const float f = limit[nt][i] == -INFINITY ? 0.0f : ex2(-nbase[nt][i] - top);
-        float* dst = red_of(warp, stage) + r * L::kRedStride + g * (D / 8);
-#pragma unroll
-        for (int d = 0; d < kSteps; d += 2)
-          *reinterpret_cast<float4*>(dst + 2 * d) = make_float4(o[d][nt][i] * f, o[d][nt][i + 2] * f,
-                                                                o[d + 1][nt][i] * f, o[d + 1][nt][i + 2] * f);
-      }
-    }
-    __syncthreads();
     const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
     const int row0 = job.item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
     const Range range = stored_range();
@@ -770,24 +720,41 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       if (p.lse && d == 0) p.lse[token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
     };
     float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.step > 0 ? 0 : 1)) * L::kPart;   // a CTA's first job, its last
-    for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float top = -INFINITY, sum = 0.0f;
-      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int w = 0; w < WARPS; ++w) {
-        const float mw = ml[w * kRows + r];
-        if (mw != -INFINITY) sum += ml[(WARPS + w) * kRows + r] * ex2(mw - top);
-        const float4 x = *reinterpret_cast<const float4*>(red_of(w, stage) + r * L::kRedStride + d);
-        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      __syncthreads();                              // ml is written; the eight rows before these are read
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = nt * 8 + 2 * t + i;
+        float top = -INFINITY;
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
+        const float f = limit[nt][i] == -INFINITY ? 0.0f : ex2(-nbase[nt][i] - top);
+        float* dst = red_of(warp, stage) + (2 * t + i) * L::kRedStride + g * (D / 8);
+#pragma unroll
+        for (int d = 0; d < kSteps; d += 2)
+          *reinterpret_cast<float4*>(dst + 2 * d) = make_float4(o[d][nt][i] * f, o[d][nt][i + 2] * f,
+                                                                o[d + 1][nt][i] * f, o[d + 1][nt][i + 2] * f);
       }
-      if (!split) {
-        finish(r, d, v, top, sum);
-      } else {
-        __stcg(reinterpret_cast<float4*>(slot + r * D + d), v);
-        if (d == 0) {
-          __stcg(slot + kRows * D + r, top);
-          __stcg(slot + kRows * (D + 1) + r, sum);
+      __syncthreads();
+      for (int i = threadIdx.x; i < min(8, rows - 8 * nt) * (D / 4); i += L::kThreads) {
+        const int r = nt * 8 + i / (D / 4), d = i % (D / 4) * 4;
+        float top = -INFINITY, sum = 0.0f;
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w * kRows + r]);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 0; w < WARPS; ++w) {
+          const float mw = ml[w * kRows + r];
+          if (mw != -INFINITY) sum += ml[(WARPS + w) * kRows + r] * ex2(mw - top);
+          const float4 x = *reinterpret_cast<const float4*>(red_of(w, stage) + (r - nt * 8) * L::kRedStride + d);
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+        if (!split) {
+          finish(r, d, v, top, sum);
+        } else {
+          __stcg(reinterpret_cast<float4*>(slot + r * D + d), v);
+          if (d == 0) {
+            __stcg(slot + kRows * D + r, top);
+            __stcg(slot + kRows * (D + 1) + r, sum);
+          }
         }
       }
     }
@@ -813,23 +780,25 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
         __threadfence();
         if (threadIdx.x == 0) *count = 0;
         const bool final = stride > 1 || groups == 1;
-        float* mls = red_of(0, stage);               // the parts' bases and sums
+        // the parts' bases and sums, over the warps' free stages
+        auto mls = [&](int c) { return red_of(c % WARPS, stage) + c / WARPS * 2 * kRows; };
         for (int i = threadIdx.x; i < n * kRows; i += L::kThreads) {
-          const float* src = part_at(from + i / kRows * stride) + kRows * D + i % kRows;
-          mls[2 * i] = __ldcg(src);
-          mls[2 * i + 1] = __ldcg(src + kRows);
+          const int c = i / kRows, r = i % kRows;
+          const float* src = part_at(from + c * stride) + kRows * D + r;
+          *reinterpret_cast<float2*>(mls(c) + 2 * r) = make_float2(__ldcg(src), __ldcg(src + kRows));
         }
         __syncthreads();
         for (int i = threadIdx.x; i < rows * (D / 4); i += L::kThreads) {
           const int r = i / (D / 4), d = i % (D / 4) * 4;
           float top = -INFINITY, sum = 0.0f;
-          for (int c = 0; c < n; ++c) top = fmaxf(top, mls[2 * (c * kRows + r)]);
+          for (int c = 0; c < n; ++c) top = fmaxf(top, mls(c)[2 * r]);
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
           for (int c = 0; c < n; ++c) {
             const float4 x = __ldcg(reinterpret_cast<const float4*>(part_at(from + c * stride)) + i);
-            const float mc = mls[2 * (c * kRows + r)], f = mc == -INFINITY ? 0.0f : ex2(mc - top);
-            sum += mls[2 * (c * kRows + r) + 1] * f;
+            const float2 ml2 = *reinterpret_cast<const float2*>(mls(c) + 2 * r);
+            const float f = ml2.x == -INFINITY ? 0.0f : ex2(ml2.x - top);
+            sum += ml2.y * f;
             v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
           }
           if (final) {

@@ -75,6 +75,12 @@ __device__ __forceinline__ Unit unit_of(const AttnParams& p, int u) {
 // kernel for few rows: here an item's pipeline fills and its sums are written.
 constexpr int kOver = 2;
 
+// A part joined costs about 3 us (the parts of an item are read by its last CTA alone), a step 2 us once the pipeline
+// is full: where there are few steps a CTA takes at least kLeast of them (256 rows of 8 heads over 2000 keys: 54 -> 35
+// us, over 4096: 67 -> 51), and where there are few items each is left to one CTA whose steps take at most kJoinCost
+// longer than an even share (256 rows over 500 keys: 27 -> 22 us, 2000 rows over 2000: 53 -> 47).
+constexpr int kLeast = 4, kJoinCost = 12;
+
 struct Job {
   Unit x;
   int u, head, step, steps;
@@ -199,15 +205,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   uint64_t *q_full = bars, *s_full = bars + 2, *p_full = bars + 4, *o_full = bars + 6;
   uint64_t *k_full = bars + 8, *k_empty = bars + 10, *v_full = bars + 12, *v_empty = bars + 14, *drain = bars + 16;
   int64_t* misc = reinterpret_cast<int64_t*>(smem + L::kBar + 176);     // the warps' sums
-  int* flags = reinterpret_cast<int*>(smem + L::kBar + 176 + 18 * 8);
+  int* flags = reinterpret_cast<int*>(smem + L::kBar + 176 + 19 * 8);
   volatile int* abort = flags;
   int* njobs = flags + 1;
+  int* longest_of = flags + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(flags + 4);
   float* qscales = reinterpret_cast<float*>(smem + L::kScaleOff);
   const int warp = threadIdx.x >> 5, lane = lane_id();
 
   if (threadIdx.x == 0) {
     *abort = 0;
+    *longest_of = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
@@ -227,13 +235,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
   // ---- this CTA's range of the list: a scan over the (sequence, row tile) units ----
   const int units = p.B * p.row_tiles;
+  // (steps in the low 40 bits, items above: both are bounded by the host)
   int64_t total = 0, before = 0, mine = 0;
+  int longest = 0;
   auto scan = [&](int base) {
     const int u = base + static_cast<int>(threadIdx.x);
     mine = 0;
     if (u < units) {
       const int steps = unit_of(p, u).steps;
-      if (steps > 0) mine = static_cast<int64_t>(steps + kOver) * p.c.heads;
+      if (steps > 0) mine = (steps + kOver + kOneItem) * p.c.heads;
+      longest = max(longest, steps);
     }
     int64_t v = mine;
 #pragma unroll
@@ -253,10 +264,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     return all;
   };
   for (int base = 0; base < units; base += kThreads) total += scan(base);
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  if (lane == 0) atomicMax(longest_of, longest);
+  __syncthreads();
+  longest = *longest_of;
+  const int items = static_cast<int>(total >> 40);
+  const int64_t everything = total;
+  total &= kOneItem - 1;
+  const int ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), total / kLeast)));
   Range range;
-  range.q = quotient(total, gridDim.x);
-  range.r = total - range.q * gridDim.x;
-  const int64_t begin = range.begin(blockIdx.x), end = range.begin(blockIdx.x + 1);
+  range.q = quotient(total, ctas);
+  range.r = total - range.q * ctas;
+  const bool by_item = items <= static_cast<int>(gridDim.x) && longest + kOver <= range.q + kJoinCost;
+  if (static_cast<int>(blockIdx.x) >= (by_item ? items : ctas)) return;
+  const int64_t begin = by_item ? static_cast<int64_t>(blockIdx.x) : range.begin(blockIdx.x);
+  const int64_t end = by_item ? begin + 1 : range.begin(blockIdx.x + 1);
   if (begin == end) return;
   if (warp == 12) {
     tmem_alloc(tmem_slot, 512);
@@ -265,18 +287,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   {
     int64_t ahead = 0;
     for (int base = 0; base < units; base += kThreads) {
-      const int64_t all = units <= kThreads ? total : scan(base);
-      if (begin >= ahead && begin < ahead + all) {
-        const int64_t at = begin - ahead - before;
-        if (at >= 0 && at < mine) {                  // the first job is this thread's
+      const int64_t all = units <= kThreads ? everything : scan(base), all_w = by_item ? all >> 40 : all & (kOneItem - 1);
+      if (begin >= ahead && begin < ahead + all_w) {
+        const int64_t at = begin - ahead - (by_item ? before >> 40 : before & (kOneItem - 1));
+        if (at >= 0 && at < (by_item ? mine >> 40 : mine & (kOneItem - 1))) {      // the first job is this thread's
           const int u = base + static_cast<int>(threadIdx.x);
           const Unit x = unit_of(p, u);
-          const int head = static_cast<int>(quotient(at, x.steps + kOver)), off = static_cast<int>(at - static_cast<int64_t>(head) * (x.steps + kOver));
-          make_job(x, u, head, max(0, off - kOver), begin + max(0, kOver - off), end, jobs);
+          const int steps = x.steps + kOver, head = static_cast<int>(by_item ? at : quotient(at, steps));
+          const int off = by_item ? kOver : static_cast<int>(at - static_cast<int64_t>(head) * steps);
+          make_job(x, u, head, max(0, off - kOver), begin + max(0, kOver - off), by_item ? begin + x.steps : end, jobs);
+          misc[18] = by_item ? begin + x.steps : end;
         }
         break;
       }
-      ahead += all;
+      ahead += all_w;
     }
   }
   if (threadIdx.x == 0) {
@@ -289,13 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
   const bool none = jobs[0].steps <= 0;              // the range lies ahead of an item's first step
   // What a role needs between items only is read back from shared memory there, not held in registers.
-  const volatile int64_t* kept = misc;               // range.q, range.r
-  auto range_end = [&]() {
-    Range k;
-    k.q = kept[16];
-    k.r = kept[17];
-    return k.begin(blockIdx.x + 1);
-  };
+  const volatile int64_t* kept = misc;               // range.q, range.r, this CTA's end
+  auto range_end = [&]() { return kept[18]; };
 
   // counts of what a role has waited for, over all jobs
   int tiles = 0;                 // key tiles (widening warps, product warp)
@@ -482,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
             if (p.lse && real) p.lse[out_token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
             tc_fence_before();
-          } else {
+          } else if (!idle) {
             // A part: [D / 4][256] float4 (coalesced over the rows), the bases, the sums.  Every warp joins its own 32
             // rows: the last CTA's warp to get here, in CTA order.
             const int64_t i0 = job.s - job.step, i1 = i0 + job.x.steps;  // the item's steps in the list

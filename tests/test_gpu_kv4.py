@@ -425,6 +425,17 @@ def test_attention_is_deterministic_and_leaves_its_workspace_zero(rows, Hq):
     b.check(*first, only=[2, 3])
 
 
+@pytest.mark.parametrize("rows", [1, 8])
+def test_attention_one_long_item_over_all_ctas_and_another_behind_it(rows):
+    """Hundreds of parts joined while the CTA that joins them has the next item's keys on their way."""
+    b = Batch([130_000, 260, 200], [rows] * 3, 4, 1, 64, 64, seed=12)
+    first = b.call()
+    b.check(*first)
+    for _ in range(20):
+        again = b.call()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_attention_bad_lengths_and_pages_are_reported():
     """A bad index on the device leads nowhere: the error word names it, the other sequences are right."""
     b = Batch([100, 200, 300], [1, 1, 1], 8, 2, 128, 32, seed=4)
