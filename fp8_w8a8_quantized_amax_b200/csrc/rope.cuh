@@ -101,13 +101,15 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ P
 // bytes), with their first loads already on the way.  A unit is eight pairs:
 // two 16-byte vectors, R / 2 apart (half layout) or side by side (interleaved).
 // A thread walks the units u, u + 256, ... of the CTA's (token, head, unit)
-// list, one at a time: the loads in flight come from six CTAs an SM (40
-// registers), which beat two units a thread with four CTAs (32.4 against
-// 35.7 us for 8192 tokens of 8 + 32 heads of 128) and loads one step ahead.
-
+// list, one at a time: the loads in flight come from eight CTAs an SM (32
+// registers; the interleaved layout needs a few more, so six: 3.5 against 3.8
+// us for 777 tokens of 13 heads of 64), which beat two units a thread with four
+// CTAs and loads one step ahead.  8192 tokens of 8 + 32 heads of 128 take 28.5
+// us, 5.9 TB/s (four tokens a CTA; 33.8 us with eight).
 template <bool INTERLEAVED>
-__global__ void __launch_bounds__(256, 6) rope_vec_kernel(const __grid_constant__ Params p, int tokens) {
-  extern __shared__ float2 table[];                 // [tokens][R / 2]
+__global__ void __launch_bounds__(256, INTERLEAVED ? 6 : 8) rope_vec_kernel(const __grid_constant__ Params p, int tokens) {
+  // [tokens][4][U][2] (cos, sin): pairs 2j and 2j + 1 of neighbouring units side by side, so that lanes read other banks
+  extern __shared__ float2 table[];
   griddep_wait();
   griddep_launch_dependents();
   const int half = p.R / 2, U = p.R / 16;
@@ -136,17 +138,19 @@ __global__ void __launch_bounds__(256, 6) rope_vec_kernel(const __grid_constant_
     }
     if (first) {                                    // the angles, while the first loads are on their way
       first = false;
-      for (int j = threadIdx.x; j < nt * half; j += 256)
-        table[j] = cos_sin(p.pos[t0 + j / half], p.freq[j % half], p.m, p.inverse != 0);
+      for (int j = threadIdx.x; j < nt * half; j += 256) {
+        const int t = j / half, f = j - t * half;
+        table[t * half + (f / 2 % 4 * U + f / 8) * 2 + f % 2] = cos_sin(p.pos[t0 + t], p.freq[f], p.m, p.inverse != 0);
+      }
       __syncthreads();
     }
     if (i >= list) break;
-    const float4* cs = reinterpret_cast<const float4*>(table + w.t * half + 8 * w.u);
+    const float4* cs = reinterpret_cast<const float4*>(table + w.t * half) + w.u;
     const uint32_t a[4] = {v0.x, v0.y, v0.z, v0.w}, b[4] = {v1.x, v1.y, v1.z, v1.w};
     uint32_t ya[4], yb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float4 c = cs[j];                       // pairs 2j and 2j + 1: (cos, sin) each
+      const float4 c = cs[j * U];                   // pairs 2j and 2j + 1: (cos, sin) each
       if constexpr (INTERLEAVED) {
         const uint32_t q0 = j < 2 ? a[2 * j] : b[2 * j - 4], q1 = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
         const float x0 = bf16lo(q0), x1 = bf16hi(q0), x2 = bf16lo(q1), x3 = bf16hi(q1);
