@@ -381,7 +381,7 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   // No more CTAs than there can be steps of 128 keys: CTAs without work are not free, and where they fill the SMs the
   // few that have some come to share an SM (64 rows of 8 heads over 500 keys: 16 -> 12 us).
   int64_t keys = max_pages * cache->page_size;
-  if (window > 0 && keys > window + p.max_q + 128) keys = window + p.max_q + 128;
+  if (window > 0 && window < keys - p.max_q - 128) keys = window + p.max_q + 128;
   const int64_t steps = items * ((keys + 127) / 128 + 1);
   const int ctas = static_cast<int>(plan.ctas < steps ? plan.ctas : steps);
   if (cache->head_dim == 128) {

@@ -111,7 +111,10 @@ __device__ __forceinline__ uint32_t encode2(float nx0, float nx1, uint64_t ny2, 
 // fp32 products a value next to a code's border could get another code than
 // its definition gives, a whole E2M1 step away.  A block's partners (half
 // layout) are read from memory as well; they are another thread's elements, so
-// they come from L1.
+// they come from L1.  8192 tokens of 8 heads of 128, four tokens a CTA: 21 us,
+// 2.0 TB/s; 65% of the issue slots are taken (quotients, conversions and the
+// fp64 rotation), which loads one step further ahead and fewer CTAs did not
+// change.  64 tokens: 2.4 us.
 template <int D>
 __global__ void __launch_bounds__(256, 4) append_kernel(const __grid_constant__ AppendParams p, int tokens) {
   constexpr int kBlocks = D / 16, kCols = D / 32;
@@ -241,7 +244,9 @@ struct ReadParams {
 };
 
 // The cached values of the given slots as bf16 (zeros for a negative slot): one
-// thread per 16 elements of one row, as many threads as there are such blocks.
+// thread per 16 elements of one row, as many threads as there are such blocks
+// (two or four a thread, loads first: 10.1 and 12.9 us where this takes 8.8, for
+// 8192 tokens of 8 heads of 128: 4.9 TB/s, partly of L2).
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const __grid_constant__ ReadParams p) {
   constexpr int kBlocks = D / 16;

@@ -167,7 +167,7 @@ __device__ __forceinline__ float pow2(int k) { return __uint_as_float(static_cas
 // into bytes (two logic operations for four values) before they are widened.
 // E2M1 times E4M3 is exact in f16.  Q is scaled by a power of two per row so
 // that its bf16 values are f16 values (all of them that are not below 2^-38 of
-// the row's largest); P, at most 1, is rounded to f16.
+// the row's largest); P, at most 2^kSlack, is rounded to f16.
 //
 // The keys of a (sequence, key head) are cut into steps of WARPS * 32; the
 // list of all steps is cut evenly over the CTAs (stream-K, as in the linear's
@@ -175,13 +175,22 @@ __device__ __forceinline__ float pow2(int k) { return __uint_as_float(static_cas
 // through its own two-stage ring of asynchronous copies and keeps its own running
 // maximum, sum and O^T; the warps' results are joined where an item ends.  An
 // item cut between CTAs is joined by the last of them to finish, in CTA order.
+//
+// Measured: 64 sequences of 410 .. 8192 keys, 32 + 8 heads of 128, one token
+// each: 76 us, 4.3 TB/s of cache (0.67 of a copy).  HBM is not what bounds it
+// there: a key's conversions, products with the scales and matrix instructions
+// keep the issue slots 62% and the ALUs 50% busy.  One token behind 131072 keys
+// (three heads to a key head): 41 us, of which the joins take about 8.  One
+// sequence of 500 keys: 8.6 us, the latency of a prologue, four steps and a join.
+// 16 sequences of four drafted tokens, 32 rows and 4096 keys: 48 us, bound like
+// the first by the instructions of two tiles of 16 rows.
 namespace few {
 
 constexpr int kTile = 32;     // keys of a warp per step
 constexpr int kStages = 2;
 constexpr int kJoin = 16;     // parts of an item joined at a time
-constexpr int kOver = 3;
-constexpr int kJoinCost = 4;  // steps that joining an item's parts takes
+constexpr int kOver = 3;      // steps that an item costs beside its keys
+constexpr int kJoinCost = 4;  // steps that joining an item's parts takes (2: 500 keys 8.8 -> 10.1 us; 8: as 4)
 
 template <int D, int NT, int WARPS>
 struct Layout {
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
   // ---- loads: the warp's tile of a step, from one page (two where pages hold 16 keys) ----
   // Nine 16-byte copies a lane at D = 128: four of K's codes, four of V's, one of the scales (lanes 0 .. 15 K's, the
   // others V's).  Bulk copies would need one instruction per run, issued lane by lane: with four runs a tile they
-  // took as many issue slots as the products (measured: 95 us against 75 us on 64 ragged sequences of up to 8192 keys).
+  // took as many issue slots as the products (95 us against 89 us then, on 64 ragged sequences of up to 8192 keys).
   uint8_t* stages = smem + warp * kStages * L::kStageBytes;
   const uint32_t slab = static_cast<uint32_t>(p.c.slab()), page_bytes = slab * p.c.heads;
   constexpr int kLoads = L::kCodes / 512;           // 16-byte copies a lane for one tensor's codes
@@ -440,64 +449,64 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
     const volatile Job& job = jobs[which];
     bool more;
     {
-    const Range range = stored_range();
-    const int64_t end = range.begin(blockIdx.x + 1);
-    more = range.q >= 0 && job.s + job.steps + kOver < end;      // (q < 0: one item a CTA)
-    if (more && threadIdx.x == 0)                    // (then this job ends its item)
-      make_job<kRows, kStep>(p, job.b, job.item + 1, 0, job.s + job.steps + kOver, end, &jobs[which ^ 1]);
+      const Range range = stored_range();
+      const int64_t end = range.begin(blockIdx.x + 1);
+      more = range.q >= 0 && job.s + job.steps + kOver < end;      // (q < 0: one item a CTA)
+      if (more && threadIdx.x == 0)                    // (then this job ends its item)
+        make_job<kRows, kStep>(p, job.b, job.item + 1, 0, job.s + job.steps + kOver, end, &jobs[which ^ 1]);
     }
     const int hi = job.x.hi, lo = job.x.first, steps = job.steps, head = job.item % p.c.heads;
     int all_first, all_last;                        // keys that every row of the item sees
     {
-    const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
-    const int row0 = job.item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
-    all_last = visible_last(p, seq, seq.kv - seq.n + row0 / p.group);
-    all_first = visible_first(p, seq.kv - seq.n + (row0 + rows - 1) / p.group);
+      const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
+      const int row0 = job.item / p.c.heads * kRows, rows = min(kRows, seq.n * p.group - row0);
+      all_last = visible_last(p, seq, seq.kv - seq.n + row0 / p.group);
+      all_first = visible_first(p, seq.kv - seq.n + (row0 + rows - 1) / p.group);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      // lane (g, t) holds row 8 nt + g, elements [t D/4, (t + 1) D/4)
-      const int r = nt * 8 + g;
-      uint32_t w[D / 8];
-      if (r < rows) {
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(smem + L::kRaw + which * L::kRawBytes) + r * D + t * (D / 4);
+      for (int nt = 0; nt < NT; ++nt) {
+        // lane (g, t) holds row 8 nt + g, elements [t D/4, (t + 1) D/4)
+        const int r = nt * 8 + g;
+        uint32_t w[D / 8];
+        if (r < rows) {
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(smem + L::kRaw + which * L::kRawBytes) + r * D + t * (D / 4);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
-          w[4 * i] = v.x;
-          w[4 * i + 1] = v.y;
-          w[4 * i + 2] = v.z;
-          w[4 * i + 3] = v.w;
+          for (int i = 0; i < D / 32; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) w[i] = 0;
         }
-      } else {
+        float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) w[i] = 0;
+        for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const int k = row_exponent(amax);
+        const float up = pow2(k), down = fmaxf(pow2(-k) * p.scale, kLeastScale);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const uint32_t b0 = pack_f16x2(bf16lo(w[2 * i]) * up, bf16hi(w[2 * i]) * up);
+          const uint32_t b1 = pack_f16x2(bf16lo(w[2 * i + 1]) * up, bf16hi(w[2 * i + 1]) * up);
+          if (warp == nt % WARPS) qs[(nt * kSteps + i) * 32 + lane] = make_uint2(b0, b1);
+        }
+        qscale[nt][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
+        qscale[nt][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          nbase[nt][i] = 0.0f;
+          limit[nt][i] = -INFINITY;
+          l[nt][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
       }
-      float amax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      const int k = row_exponent(amax);
-      const float up = pow2(k), down = fmaxf(pow2(-k) * p.scale, kLeastScale);
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const uint32_t b0 = pack_f16x2(bf16lo(w[2 * i]) * up, bf16hi(w[2 * i]) * up);
-        const uint32_t b1 = pack_f16x2(bf16lo(w[2 * i + 1]) * up, bf16hi(w[2 * i + 1]) * up);
-        if (warp == nt % WARPS) qs[(nt * kSteps + i) * 32 + lane] = make_uint2(b0, b1);
-      }
-      qscale[nt][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
-      qscale[nt][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        nbase[nt][i] = 0.0f;
-        limit[nt][i] = -INFINITY;
-        l[nt][i] = 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
-    }
     }
     const int32_t* table = p.table + job.b * p.table_stride;
     int key = job.key + warp * kTile;

@@ -16,9 +16,18 @@
 // Roles: warps 0-3 and 4-7 softmax of tile 0 and 1, warps 8-11 widening, warp 12
 // issues the products.  A softmax warp brings its 32 rows' queries of the next
 // item as soon as the last S of the item before is done, ahead of that item's
-// end.  Tensor memory (512 columns): S0, S1 (P over the first half of S), O0, O1.  The list of (256 rows, key head) items, each with its own
-// run of 128-key steps, is cut evenly over the CTAs as in the kernel for few
-// rows; parts of a cut item are joined by the last of its CTAs, in CTA order.
+// end.  Tensor memory (512 columns): S0, S1 (P over the first half of S), O0,
+// O1.  The list of (256 rows, key head) items, each with its own run of 128-key
+// steps, is cut over the CTAs as in the kernel for few rows; parts of a cut item
+// are joined by the last of its CTAs, in CTA order.
+//
+// Measured: 2048 new tokens of 32 heads behind 6144 cached ones (8 key heads, D =
+// 128): 240 us, 1.0 PFLOP/s of the visible products (0.61 of what a library
+// product reaches).  A step of 256 rows takes 3.9 K cycles where its products
+// take 2.05 K: a tile's chain S, maximum, exponentials, P . V is longer than the
+// other tile's share of the tensor cores, and a row's two passes over tensor
+// memory by one thread are its longest link.  Sixteen softmax warps (one pass, S
+// held in registers) spilled and were slower.
 #pragma once
 
 #include "kv4_attention.cuh"
@@ -357,310 +366,310 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   if (none) {
   } else if (warp < 8) {
     for (;;) {
-        // ----------------------------------------------------------- softmax ---
-        const int w = warp >> 2, r = threadIdx.x & 127;
-        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // 32 lanes a warp
-        const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + 256 + w * 128;
-        // This warp's 32 rows of an item's queries: a row by D / 8 lanes, 16 bytes each, all on their way at once; scaled
-        // to f16, into the swizzled operand tile.
-        auto bring_queries = [&](const Job& job) {
-          constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-          const int c = lane % kLanes, first = (warp & 3) * 32 + lane / kLanes;
-          uint4 v[kLanes];
-          const int row = job.x.row0 + w * 128 + first, dt = kAtOnce / p.group, dh = kAtOnce - dt * p.group;
-          int t = row / p.group, h = row - t * p.group;
-          const uint16_t* src = p.q + static_cast<int64_t>(job.x.s.r0) * p.qt + static_cast<int64_t>(job.head) * p.group * p.qh + 8 * c;
+      // ----------------------------------------------------------- softmax ---
+      const int w = warp >> 2, r = threadIdx.x & 127;
+      const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // 32 lanes a warp
+      const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + 256 + w * 128;
+      // This warp's 32 rows of an item's queries: a row by D / 8 lanes, 16 bytes each, all on their way at once; scaled
+      // to f16, into the swizzled operand tile.
+      auto bring_queries = [&](const Job& job) {
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+        const int c = lane % kLanes, first = (warp & 3) * 32 + lane / kLanes;
+        uint4 v[kLanes];
+        const int row = job.x.row0 + w * 128 + first, dt = kAtOnce / p.group, dh = kAtOnce - dt * p.group;
+        int t = row / p.group, h = row - t * p.group;
+        const uint16_t* src = p.q + static_cast<int64_t>(job.x.s.r0) * p.qt + static_cast<int64_t>(job.head) * p.group * p.qh + 8 * c;
 #pragma unroll
-          for (int u = 0; u < kLanes; ++u) {
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (w * 128 + first + u * kAtOnce < job.x.rows) v[u] = *reinterpret_cast<const uint4*>(src + t * p.qt + h * p.qh);
-            t += dt;
-            h += dh;
-            if (h >= p.group) {
-              h -= p.group;
-              ++t;
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kLanes; ++u) {
-            const int r = first + u * kAtOnce;
-            const uint32_t a[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            float amax = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(a[e])), fabsf(bf16hi(a[e]))));
-#pragma unroll
-            for (int o = 1; o < kLanes; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            const int k = row_exponent(amax);
-            const float up = pow2(k);
-            uint32_t f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = pack_f16x2(bf16lo(a[e]) * up, bf16hi(a[e]) * up);
-            *reinterpret_cast<uint4*>(smem + L::kQ + w * L::kTile + c / 8 * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                make_uint4(f[0], f[1], f[2], f[3]);
-            if (c == 0) qscales[w * 128 + r] = fmaxf(pow2(-k) * p.scale, kLeastScale);
-          }
-          fence_proxy_async_smem();
-          warp_arrive(&q_full[w]);
-        };
-        const bool first_mine = w * 128 < jobs[0].x.rows;
-        if (first_mine) bring_queries(jobs[0]);
-        meet_all();
-        const int n = *njobs;
-        auto next_job = [&](int i) {                 // the next item with rows of this tile
-          while (i < n && w * 128 >= jobs[i].x.rows) ++i;
-          return i;
-        };
-        bool ok = true;
-        int i = next_job(0);
-        if (!first_mine && i < n) bring_queries(jobs[i]);
-        for (int following; i < n && ok; i = following) {
-          const volatile Job& job = jobs[i];
-          following = next_job(i + 1);
-          const float qscale = qscales[w * 128 + r];   // (written by this warp)
-          const bool idle = w * 128 + (r & ~31) >= job.x.rows;
-          int vfirst, vlast;
-          {
-            const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
-            const int pos = seq.kv - seq.n + (job.x.row0 + min(w * 128 + r, job.x.rows - 1)) / p.group;
-            vfirst = visible_first(p, pos);
-            vlast = visible_last(p, seq, pos);
-          }
-          float nbase = 0.0f, limit = -INFINITY, sum = 0.0f;
-          int key = job.x.lo + job.step * kKeys;
-          const int steps = job.steps;
-          for (int j = 0; j < steps; ++j, key += kKeys, ++turns) {
-            ok = mbar_spin(&s_full[w], turns & 1, abort, kErrWaitTmemFull);
-            if (!ok) break;
-            tc_fence_after();
-            if (idle) {                                // none of this warp's rows is one: what they hold is never read
-              tc_fence_before();
-              warp_arrive(&p_full[w]);
-              continue;
-            }
-            const int first = vfirst - key, last = vlast - key;
-            if (!__all_sync(0xFFFFFFFFu, first <= 0 && last >= kKeys)) row_mask(ts, first, last);
-            const float top = row_max(ts);
-            if (__any_sync(0xFFFFFFFFu, top > limit)) {
-              const float was = limit == -INFINITY ? -INFINITY : -nbase, now = fmaxf(was, top * qscale);
-              float f = 1.0f;
-              if (now > was) {
-                f = ex2(was - now);                    // 0 from -infinity
-                nbase = -now;
-                limit = (now + kSlack) / qscale;
-                sum *= f;
-              }
-              if (j > 0) {                             // S of this step was issued after O's last product: O is at rest
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                  uint32_t o[32];
-                  tmem_ld_32x32b_x32(to + 32 * c, o);
-                  tmem_ld_wait_regs(o);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st_32x32b_x32(to + 32 * c, o);
-                }
-              }
-            }
-            sum += row_exp(ts, qscale, nbase);
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&p_full[w]);
-          }
-          if (!ok) break;
-          __syncwarp();
-          if (following < n) bring_queries(jobs[following]);
-          ok = mbar_wait(&o_full[w], done & 1, abort, kErrWaitTmemFull);
-          if (!ok) break;
-          ++done;
-          tc_fence_after();
-          // ---- the item's end ----
-          const float top = limit == -INFINITY ? -INFINITY : -nbase;
-          if (limit == -INFINITY) sum = 0.0f;        // no visible key (the polynomial's least value is not zero)
-          const bool real = w * 128 + r < job.x.rows;
-          const int row = job.x.row0 + w * 128 + r, token = row / p.group, h = job.head * p.group + row - token * p.group;
-          const int64_t out_token = job.x.s.r0 + static_cast<int64_t>(token);
-          uint16_t* out = p.o + out_token * p.ot + h * p.oh;
-          if (job.steps == job.x.steps) {
-            const float f = sum > 0.0f ? p.c.vg / sum : 0.0f;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + 32 * c, o);
-              tmem_ld_wait_regs(o);
-              if (real) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint4 v;
-                  v.x = pack_bf16x2(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f);
-                  v.y = pack_bf16x2(__uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
-                  v.z = pack_bf16x2(__uint_as_float(o[e + 4]) * f, __uint_as_float(o[e + 5]) * f);
-                  v.w = pack_bf16x2(__uint_as_float(o[e + 6]) * f, __uint_as_float(o[e + 7]) * f);
-                  *reinterpret_cast<uint4*>(out + 32 * c + e) = v;
-                }
-              }
-            }
-            if (p.lse && real) p.lse[out_token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
-            tc_fence_before();
-          } else if (!idle) {
-            // A part: [D / 4][256] float4 (coalesced over the rows), the bases, the sums.  Every warp joins its own 32
-            // rows: the last CTA's warp to get here, in CTA order.
-            const int64_t i0 = job.s - job.step, i1 = i0 + job.x.steps;  // the item's steps in the list
-            Range range;
-            range.q = kept[16];
-            range.r = kept[17];
-            const int row_in = w * 128 + r;
-            float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.step > 0 ? 0 : 1)) * L::kPart;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + 32 * c, o);
-              tmem_ld_wait_regs(o);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                __stcg(reinterpret_cast<float4*>(slot) + (8 * c + e) * kRows + row_in,
-                       make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
-                                   __uint_as_float(o[4 * e + 3])));
-            }
-            tc_fence_before();
-            __stcg(slot + kRows * D + row_in, top);
-            __stcg(slot + kRows * (D + 1) + row_in, sum);
-            const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
-            unsigned* count = p.count + c0 * 8 + warp;
-            __threadfence();
-            __syncwarp();
-            unsigned arrived = 0;
-            if (lane == 0) arrived = atom_add_acq_rel_gpu(count, 1u);
-            arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
-            if (arrived == static_cast<unsigned>(parts - 1)) {
-              __threadfence();
-              if (lane == 0) *count = 0;
-              const float* at0 = p.part + (2 * static_cast<int64_t>(c0) + 1) * L::kPart;
-              const float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
-              auto part = [&](int c) { return c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart; };
-              float m = -INFINITY, l = 0.0f;
-#pragma unroll 4
-              for (int c = 0; c < parts; ++c) m = fmaxf(m, __ldcg(part(c) + kRows * D + row_in));
-              auto share = [&](int c) {              // a part's factor
-                const float mc = __ldcg(part(c) + kRows * D + row_in);
-                return mc == -INFINITY ? 0.0f : ex2(mc - m);
-              };
-#pragma unroll 4
-              for (int c = 0; c < parts; ++c) l += __ldcg(part(c) + kRows * (D + 1) + row_in) * share(c);
-              const float f = l > 0.0f ? p.c.vg / l : 0.0f;
-#pragma unroll
-              for (int e = 0; e < D / 32; ++e) {     // 32 columns: eight loads on their way
-                float4 a[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-                for (int c = 0; c < parts; ++c) {
-                  float4 v[8];
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(part(c)) + (8 * e + k) * kRows + row_in);
-                  const float g = share(c);
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    a[k].x += v[k].x * g; a[k].y += v[k].y * g; a[k].z += v[k].z * g; a[k].w += v[k].w * g;
-                  }
-                }
-                if (real) {
-#pragma unroll
-                  for (int k = 0; k < 8; k += 2)
-                    *reinterpret_cast<uint4*>(out + 32 * e + 4 * k) =
-                        make_uint4(pack_bf16x2(a[k].x * f, a[k].y * f), pack_bf16x2(a[k].z * f, a[k].w * f),
-                                   pack_bf16x2(a[k + 1].x * f, a[k + 1].y * f), pack_bf16x2(a[k + 1].z * f, a[k + 1].w * f));
-                }
-              }
-              if (p.lse && real) p.lse[out_token * p.Hq + h] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
-            }
+        for (int u = 0; u < kLanes; ++u) {
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (w * 128 + first + u * kAtOnce < job.x.rows) v[u] = *reinterpret_cast<const uint4*>(src + t * p.qt + h * p.qh);
+          t += dt;
+          h += dh;
+          if (h >= p.group) {
+            h -= p.group;
+            ++t;
           }
         }
+#pragma unroll
+        for (int u = 0; u < kLanes; ++u) {
+          const int r = first + u * kAtOnce;
+          const uint32_t a[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          float amax = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16lo(a[e])), fabsf(bf16hi(a[e]))));
+#pragma unroll
+          for (int o = 1; o < kLanes; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          const int k = row_exponent(amax);
+          const float up = pow2(k);
+          uint32_t f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = pack_f16x2(bf16lo(a[e]) * up, bf16hi(a[e]) * up);
+          *reinterpret_cast<uint4*>(smem + L::kQ + w * L::kTile + c / 8 * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+          if (c == 0) qscales[w * 128 + r] = fmaxf(pow2(-k) * p.scale, kLeastScale);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&q_full[w]);
+      };
+      const bool first_mine = w * 128 < jobs[0].x.rows;
+      if (first_mine) bring_queries(jobs[0]);
+      meet_all();
+      const int n = *njobs;
+      auto next_job = [&](int i) {                 // the next item with rows of this tile
+        while (i < n && w * 128 >= jobs[i].x.rows) ++i;
+        return i;
+      };
+      bool ok = true;
+      int i = next_job(0);
+      if (!first_mine && i < n) bring_queries(jobs[i]);
+      for (int following; i < n && ok; i = following) {
+        const volatile Job& job = jobs[i];
+        following = next_job(i + 1);
+        const float qscale = qscales[w * 128 + r];   // (written by this warp)
+        const bool idle = w * 128 + (r & ~31) >= job.x.rows;
+        int vfirst, vlast;
+        {
+          const Seq seq = {job.x.s.r0, job.x.s.n, job.x.s.kv};
+          const int pos = seq.kv - seq.n + (job.x.row0 + min(w * 128 + r, job.x.rows - 1)) / p.group;
+          vfirst = visible_first(p, pos);
+          vlast = visible_last(p, seq, pos);
+        }
+        float nbase = 0.0f, limit = -INFINITY, sum = 0.0f;
+        int key = job.x.lo + job.step * kKeys;
+        const int steps = job.steps;
+        for (int j = 0; j < steps; ++j, key += kKeys, ++turns) {
+          ok = mbar_spin(&s_full[w], turns & 1, abort, kErrWaitTmemFull);
+          if (!ok) break;
+          tc_fence_after();
+          if (idle) {                                // none of this warp's rows is one: what they hold is never read
+            tc_fence_before();
+            warp_arrive(&p_full[w]);
+            continue;
+          }
+          const int first = vfirst - key, last = vlast - key;
+          if (!__all_sync(0xFFFFFFFFu, first <= 0 && last >= kKeys)) row_mask(ts, first, last);
+          const float top = row_max(ts);
+          if (__any_sync(0xFFFFFFFFu, top > limit)) {
+            const float was = limit == -INFINITY ? -INFINITY : -nbase, now = fmaxf(was, top * qscale);
+            float f = 1.0f;
+            if (now > was) {
+              f = ex2(was - now);                    // 0 from -infinity
+              nbase = -now;
+              limit = (now + kSlack) / qscale;
+              sum *= f;
+            }
+            if (j > 0) {                             // S of this step was issued after O's last product: O is at rest
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(to + 32 * c, o);
+                tmem_ld_wait_regs(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st_32x32b_x32(to + 32 * c, o);
+              }
+            }
+          }
+          sum += row_exp(ts, qscale, nbase);
+          tmem_st_wait();
+          tc_fence_before();
+          warp_arrive(&p_full[w]);
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (following < n) bring_queries(jobs[following]);
+        ok = mbar_wait(&o_full[w], done & 1, abort, kErrWaitTmemFull);
+        if (!ok) break;
+        ++done;
+        tc_fence_after();
+        // ---- the item's end ----
+        const float top = limit == -INFINITY ? -INFINITY : -nbase;
+        if (limit == -INFINITY) sum = 0.0f;        // no visible key (the polynomial's least value is not zero)
+        const bool real = w * 128 + r < job.x.rows;
+        const int row = job.x.row0 + w * 128 + r, token = row / p.group, h = job.head * p.group + row - token * p.group;
+        const int64_t out_token = job.x.s.r0 + static_cast<int64_t>(token);
+        uint16_t* out = p.o + out_token * p.ot + h * p.oh;
+        if (job.steps == job.x.steps) {
+          const float f = sum > 0.0f ? p.c.vg / sum : 0.0f;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 32 * c, o);
+            tmem_ld_wait_regs(o);
+            if (real) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint4 v;
+                v.x = pack_bf16x2(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f);
+                v.y = pack_bf16x2(__uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+                v.z = pack_bf16x2(__uint_as_float(o[e + 4]) * f, __uint_as_float(o[e + 5]) * f);
+                v.w = pack_bf16x2(__uint_as_float(o[e + 6]) * f, __uint_as_float(o[e + 7]) * f);
+                *reinterpret_cast<uint4*>(out + 32 * c + e) = v;
+              }
+            }
+          }
+          if (p.lse && real) p.lse[out_token * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+          tc_fence_before();
+        } else if (!idle) {
+          // A part: [D / 4][256] float4 (coalesced over the rows), the bases, the sums.  Every warp joins its own 32
+          // rows: the last CTA's warp to get here, in CTA order.
+          const int64_t i0 = job.s - job.step, i1 = i0 + job.x.steps;  // the item's steps in the list
+          Range range;
+          range.q = kept[16];
+          range.r = kept[17];
+          const int row_in = w * 128 + r;
+          float* slot = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (job.step > 0 ? 0 : 1)) * L::kPart;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 32 * c, o);
+            tmem_ld_wait_regs(o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              __stcg(reinterpret_cast<float4*>(slot) + (8 * c + e) * kRows + row_in,
+                     make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                 __uint_as_float(o[4 * e + 3])));
+          }
+          tc_fence_before();
+          __stcg(slot + kRows * D + row_in, top);
+          __stcg(slot + kRows * (D + 1) + row_in, sum);
+          const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
+          unsigned* count = p.count + c0 * 8 + warp;
+          __threadfence();
+          __syncwarp();
+          unsigned arrived = 0;
+          if (lane == 0) arrived = atom_add_acq_rel_gpu(count, 1u);
+          arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
+          if (arrived == static_cast<unsigned>(parts - 1)) {
+            __threadfence();
+            if (lane == 0) *count = 0;
+            const float* at0 = p.part + (2 * static_cast<int64_t>(c0) + 1) * L::kPart;
+            const float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
+            auto part = [&](int c) { return c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart; };
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+            for (int c = 0; c < parts; ++c) m = fmaxf(m, __ldcg(part(c) + kRows * D + row_in));
+            auto share = [&](int c) {              // a part's factor
+              const float mc = __ldcg(part(c) + kRows * D + row_in);
+              return mc == -INFINITY ? 0.0f : ex2(mc - m);
+            };
+#pragma unroll 4
+            for (int c = 0; c < parts; ++c) l += __ldcg(part(c) + kRows * (D + 1) + row_in) * share(c);
+            const float f = l > 0.0f ? p.c.vg / l : 0.0f;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {     // 32 columns: eight loads on their way
+              float4 a[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+              for (int c = 0; c < parts; ++c) {
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(part(c)) + (8 * e + k) * kRows + row_in);
+                const float g = share(c);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  a[k].x += v[k].x * g; a[k].y += v[k].y * g; a[k].z += v[k].z * g; a[k].w += v[k].w * g;
+                }
+              }
+              if (real) {
+#pragma unroll
+                for (int k = 0; k < 8; k += 2)
+                  *reinterpret_cast<uint4*>(out + 32 * e + 4 * k) =
+                      make_uint4(pack_bf16x2(a[k].x * f, a[k].y * f), pack_bf16x2(a[k].z * f, a[k].w * f),
+                                 pack_bf16x2(a[k + 1].x * f, a[k + 1].y * f), pack_bf16x2(a[k + 1].z * f, a[k + 1].w * f));
+              }
+            }
+            if (p.lse && real) p.lse[out_token * p.Hq + h] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          }
+        }
+      }
       if (list_done(n)) break;
     }
   } else if (warp < 12) {
     for (;;) {
-        // ---------------------------------------------------------- widening ---
-        // One thread per key; the next tile's bytes are on their way while this one's are widened.
-        const int r = threadIdx.x - 256;
-        uint4 raw[2][D / 32];
-        uint2 sc[2];
-        // a key's page (-1: no such key), looked up one tile ahead of its bytes
-        auto page_of = [&](const Job& j, int step) {
-          const int key = j.x.lo + (j.step + step) * kKeys + r;
-          return key < j.x.hi && key >= j.x.first ? p.table[j.u / p.row_tiles * p.table_stride + (key >> p.c.page_shift)] : -1;
-        };
-        auto fetch = [&](const Job& j, int step, int page, int which) {
-          const int key = j.x.lo + (j.step + step) * kKeys + r;
-          const bool there = key < j.x.hi && key >= j.x.first;
+      // ---------------------------------------------------------- widening ---
+      // One thread per key; the next tile's bytes are on their way while this one's are widened.
+      const int r = threadIdx.x - 256;
+      uint4 raw[2][D / 32];
+      uint2 sc[2];
+      // a key's page (-1: no such key), looked up one tile ahead of its bytes
+      auto page_of = [&](const Job& j, int step) {
+        const int key = j.x.lo + (j.step + step) * kKeys + r;
+        return key < j.x.hi && key >= j.x.first ? p.table[j.u / p.row_tiles * p.table_stride + (key >> p.c.page_shift)] : -1;
+      };
+      auto fetch = [&](const Job& j, int step, int page, int which) {
+        const int key = j.x.lo + (j.step + step) * kKeys + r;
+        const bool there = key < j.x.hi && key >= j.x.first;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) raw[which][i] = make_uint4(0, 0, 0, 0);
-          sc[which] = make_uint2(0, 0);
-          if (there && (page < 0 || page >= p.c.pages)) atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadPage));
-          if (there && page >= 0 && page < p.c.pages) {
-            const uint8_t* base = which ? p.c.v : p.c.k;
-            const int row = key & (p.c.page_size - 1);
-            const uint4* src = reinterpret_cast<const uint4*>(base + p.c.code_offset(page, j.head, row));
+        for (int i = 0; i < D / 32; ++i) raw[which][i] = make_uint4(0, 0, 0, 0);
+        sc[which] = make_uint2(0, 0);
+        if (there && (page < 0 || page >= p.c.pages)) atomicCAS(&g_device_error, 0, static_cast<int>(kErrBadPage));
+        if (there && page >= 0 && page < p.c.pages) {
+          const uint8_t* base = which ? p.c.v : p.c.k;
+          const int row = key & (p.c.page_size - 1);
+          const uint4* src = reinterpret_cast<const uint4*>(base + p.c.code_offset(page, j.head, row));
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) raw[which][i] = src[i];
-            const uint8_t* ss = base + p.c.scale_offset(page, j.head, row);
-            if constexpr (D == 128) sc[which] = *reinterpret_cast<const uint2*>(ss);
-            else sc[which].x = *reinterpret_cast<const uint32_t*>(ss);
-          }
-        };
-        auto widen = [&](int which, uint8_t* dst) {
+          for (int i = 0; i < D / 32; ++i) raw[which][i] = src[i];
+          const uint8_t* ss = base + p.c.scale_offset(page, j.head, row);
+          if constexpr (D == 128) sc[which] = *reinterpret_cast<const uint2*>(ss);
+          else sc[which].x = *reinterpret_cast<const uint32_t*>(ss);
+        }
+      };
+      auto widen = [&](int which, uint8_t* dst) {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {           // 32 elements: two scales, four 16-byte chunks
-            const uint32_t two = widen_e4m3x2((i < 2 ? sc[which].x : sc[which].y) >> (i % 2 * 16));
-            const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
-            const uint32_t w[4] = {raw[which][i].x, raw[which][i].y, raw[which][i].z, raw[which][i].w};
+        for (int i = 0; i < D / 32; ++i) {           // 32 elements: two scales, four 16-byte chunks
+          const uint32_t two = widen_e4m3x2((i < 2 ? sc[which].x : sc[which].y) >> (i % 2 * 16));
+          const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+          const uint32_t w[4] = {raw[which][i].x, raw[which][i].y, raw[which][i].z, raw[which][i].w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t e[4];
-              widen4(w[c], e);
-              const uint32_t s = c < 2 ? s0 : s1;
-              const int chunk = 4 * (i % 2) + c;
-              *reinterpret_cast<uint4*>(dst + i / 2 * kHalf + r * 128 + ((chunk ^ (r & 7)) << 4)) =
-                  make_uint4(mul_f16x2(e[0], s), mul_f16x2(e[1], s), mul_f16x2(e[2], s), mul_f16x2(e[3], s));
-            }
-          }
-          fence_proxy_async_smem();
-        };
-        bool ok = true;
-        // tiles in turn: at (i, j) the one widened, then the one whose bytes are fetched, then the one whose page is
-        int fi = 0, fj = 0;
-        auto step_on = [&](int& i, int& j) {
-          if (++j == jobs[i].steps) {
-            j = 0;
-            ++i;
-          }
-        };
-        int page = page_of(jobs[0], 0);
-        fetch(jobs[0], 0, page, 0);
-        fetch(jobs[0], 0, page, 1);
-        meet_all();
-        const int n = *njobs;
-        step_on(fi, fj);
-        page = fi < n ? page_of(jobs[fi], fj) : -1;
-        for (int i = 0; i < n && ok; ++i) {
-          const int steps = jobs[i].steps;
-          for (int j = 0; j < steps && ok; ++j, ++tiles) {
-            const int st = tiles & 1, ph = ((tiles >> 1) & 1) ^ 1;
-            ok = mbar_wait(&k_empty[st], ph, abort, kErrWaitEmpty);
-            if (!ok) break;
-            widen(0, smem + L::kK + st * L::kTile);
-            warp_arrive(&k_full[st]);
-            if (fi < n) fetch(jobs[fi], fj, page, 0);
-            ok = mbar_wait(&v_empty[st], ph, abort, kErrWaitEmpty);
-            if (!ok) break;
-            widen(1, smem + L::kV + st * L::kTile);
-            warp_arrive(&v_full[st]);
-            if (fi < n) {
-              fetch(jobs[fi], fj, page, 1);
-              step_on(fi, fj);
-              page = fi < n ? page_of(jobs[fi], fj) : -1;
-            }
+          for (int c = 0; c < 4; ++c) {
+            uint32_t e[4];
+            widen4(w[c], e);
+            const uint32_t s = c < 2 ? s0 : s1;
+            const int chunk = 4 * (i % 2) + c;
+            *reinterpret_cast<uint4*>(dst + i / 2 * kHalf + r * 128 + ((chunk ^ (r & 7)) << 4)) =
+                make_uint4(mul_f16x2(e[0], s), mul_f16x2(e[1], s), mul_f16x2(e[2], s), mul_f16x2(e[3], s));
           }
         }
+        fence_proxy_async_smem();
+      };
+      bool ok = true;
+      // tiles in turn: at (i, j) the one widened, then the one whose bytes are fetched, then the one whose page is
+      int fi = 0, fj = 0;
+      auto step_on = [&](int& i, int& j) {
+        if (++j == jobs[i].steps) {
+          j = 0;
+          ++i;
+        }
+      };
+      int page = page_of(jobs[0], 0);
+      fetch(jobs[0], 0, page, 0);
+      fetch(jobs[0], 0, page, 1);
+      meet_all();
+      const int n = *njobs;
+      step_on(fi, fj);
+      page = fi < n ? page_of(jobs[fi], fj) : -1;
+      for (int i = 0; i < n && ok; ++i) {
+        const int steps = jobs[i].steps;
+        for (int j = 0; j < steps && ok; ++j, ++tiles) {
+          const int st = tiles & 1, ph = ((tiles >> 1) & 1) ^ 1;
+          ok = mbar_wait(&k_empty[st], ph, abort, kErrWaitEmpty);
+          if (!ok) break;
+          widen(0, smem + L::kK + st * L::kTile);
+          warp_arrive(&k_full[st]);
+          if (fi < n) fetch(jobs[fi], fj, page, 0);
+          ok = mbar_wait(&v_empty[st], ph, abort, kErrWaitEmpty);
+          if (!ok) break;
+          widen(1, smem + L::kV + st * L::kTile);
+          warp_arrive(&v_full[st]);
+          if (fi < n) {
+            fetch(jobs[fi], fj, page, 1);
+            step_on(fi, fj);
+            page = fi < n ? page_of(jobs[fi], fj) : -1;
+          }
+        }
+      }
       if (list_done(n)) break;
     }
   } else {
@@ -668,65 +677,65 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       if (lane == 0) list_jobs();
       meet_all();
       const int n = *njobs;
-        // ---------------------------------------------------------- products ---
-        constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys, false), kIdescO = idesc_f16_f32(128, D, true);
-        // descriptors of the tiles' starts: an offset is added to the address field (shared memory ends below its range)
-        const uint64_t q_desc = umma_desc_sw128(smem_u32(smem + L::kQ)), k_desc = umma_desc_sw128(smem_u32(smem + L::kK));
-        const uint64_t v_desc = umma_desc_mn_sw128(smem_u32(smem + L::kV), kHalf);
-        bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-          const int steps = jobs[i].steps, two = jobs[i].x.rows > 128 ? 2 : 1;
-          auto score = [&](int w, int tile) {          // S_w = Q_w . K_tile^T
-            const uint64_t a = q_desc + (w * L::kTile >> 4), b = k_desc + ((tile & 1) * L::kTile >> 4);
+      // ---------------------------------------------------------- products ---
+      constexpr uint32_t kIdescS = idesc_f16_f32(128, kKeys, false), kIdescO = idesc_f16_f32(128, D, true);
+      // descriptors of the tiles' starts: an offset is added to the address field (shared memory ends below its range)
+      const uint64_t q_desc = umma_desc_sw128(smem_u32(smem + L::kQ)), k_desc = umma_desc_sw128(smem_u32(smem + L::kK));
+      const uint64_t v_desc = umma_desc_mn_sw128(smem_u32(smem + L::kV), kHalf);
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const int steps = jobs[i].steps, two = jobs[i].x.rows > 128 ? 2 : 1;
+        auto score = [&](int w, int tile) {          // S_w = Q_w . K_tile^T
+          const uint64_t a = q_desc + (w * L::kTile >> 4), b = k_desc + ((tile & 1) * L::kTile >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_f16_ss(tmem + w * 128, a + ((k / 4 * kHalf + k % 4 * 32) >> 4), b + ((k / 4 * kHalf + k % 4 * 32) >> 4),
+                         kIdescS, k > 0);
+            mma_commit(&s_full[w]);
+            if (w == two - 1) mma_commit(&k_empty[tile & 1]);
+          }
+          __syncwarp();
+        };
+        for (int w = 0; w < two && ok; ++w) {
+          ok = mbar_wait(&q_full[w], (w ? done1 : done) & 1, abort, kErrWaitFull);
+          if (ok && w == 0) ok = mbar_wait(&k_full[tiles & 1], (tiles >> 1) & 1, abort, kErrWaitFull);
+          if (!ok) break;
+          tc_fence_after();
+          score(w, tiles);
+        }
+        for (int j = 0; j < steps && ok; ++j) {
+          const int tile = tiles + j;
+          ok = mbar_wait(&v_full[tile & 1], (tile >> 1) & 1, abort, kErrWaitFull);
+          for (int w = 0; w < two && ok; ++w) {
+            ok = mbar_spin(&p_full[w], (w ? turns1 : turns) & 1, abort, kErrWaitTmemFull);
+            if (!ok) break;
+            if (w) ++turns1; else ++turns;
+            tc_fence_after();
+            const uint64_t v = v_desc + ((tile & 1) * L::kTile >> 4);
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_f16_ss(tmem + w * 128, a + ((k / 4 * kHalf + k % 4 * 32) >> 4), b + ((k / 4 * kHalf + k % 4 * 32) >> 4),
-                           kIdescS, k > 0);
-              mma_commit(&s_full[w]);
-              if (w == two - 1) mma_commit(&k_empty[tile & 1]);
+              for (int k = 0; k < kKeys / 16; ++k)
+                mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, v + (k * 2048 >> 4), kIdescO,
+                           j > 0 || k > 0);
+              if (j + 1 == steps) mma_commit(&o_full[w]);
+              if (w == two - 1) mma_commit(&v_empty[tile & 1]);
             }
             __syncwarp();
-          };
-          for (int w = 0; w < two && ok; ++w) {
-            ok = mbar_wait(&q_full[w], (w ? done1 : done) & 1, abort, kErrWaitFull);
-            if (ok && w == 0) ok = mbar_wait(&k_full[tiles & 1], (tiles >> 1) & 1, abort, kErrWaitFull);
-            if (!ok) break;
-            tc_fence_after();
-            score(w, tiles);
-          }
-          for (int j = 0; j < steps && ok; ++j) {
-            const int tile = tiles + j;
-            ok = mbar_wait(&v_full[tile & 1], (tile >> 1) & 1, abort, kErrWaitFull);
-            for (int w = 0; w < two && ok; ++w) {
-              ok = mbar_spin(&p_full[w], (w ? turns1 : turns) & 1, abort, kErrWaitTmemFull);
-              if (!ok) break;
-              if (w) ++turns1; else ++turns;
-              tc_fence_after();
-              const uint64_t v = v_desc + ((tile & 1) * L::kTile >> 4);
-              if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, v + (k * 2048 >> 4), kIdescO,
-                             j > 0 || k > 0);
-                if (j + 1 == steps) mma_commit(&o_full[w]);
-                if (w == two - 1) mma_commit(&v_empty[tile & 1]);
+            if (j + 1 < steps) {
+              if (w == 0) {
+                ok = mbar_wait(&k_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1, abort, kErrWaitFull);
+                if (!ok) break;
+                tc_fence_after();
               }
-              __syncwarp();
-              if (j + 1 < steps) {
-                if (w == 0) {
-                  ok = mbar_wait(&k_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1, abort, kErrWaitFull);
-                  if (!ok) break;
-                  tc_fence_after();
-                }
-                score(w, tile + 1);
-              }
+              score(w, tile + 1);
             }
           }
-          tiles += steps;
-          ++done;
-          if (two == 2) ++done1;
         }
+        tiles += steps;
+        ++done;
+        if (two == 2) ++done1;
+      }
       if (list_done(n)) break;
     }
   }

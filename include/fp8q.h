@@ -433,7 +433,7 @@ FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* s
  *   A row that sees no key gets zeros (lse -inf).  Rows that belong to no
  *   sequence (behind q_start[B]) are left as they were.
  *   Q_bf16, O_bf16  [T, Hq, D], 16-byte aligned, strides % 8 == 0; O's rows must
- *                   not overlap.  Q's values must be finite.
+ *                   not overlap each other or Q.  Q's values must be finite.
  *   page_table      [B, max_pages] int32, row stride table_stride >= max_pages;
  *                   max_pages * page_size < 2^31 - 65536.  Entries that no visible
  *                   key needs are not read.

@@ -436,6 +436,15 @@ def test_attention_one_long_item_over_all_ctas_and_another_behind_it(rows):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("rows", [1, 8, 70])
+def test_attention_a_window_longer_than_any_context_is_none(rows):
+    b = Batch([500, 130], [rows, rows], 8, 2, 128, 32, seed=5)
+    want, lse = b.call()
+    for window in (500, 2 ** 31, 2 ** 62, 2 ** 63 - 1):
+        got = b.call(window=window)
+        assert torch.equal(got[0], want) and torch.equal(got[1], lse), window
+
+
 def test_attention_bad_lengths_and_pages_are_reported():
     """A bad index on the device leads nowhere: the error word names it, the other sequences are right."""
     b = Batch([100, 200, 300], [1, 1, 1], 8, 2, 128, 32, seed=4)
