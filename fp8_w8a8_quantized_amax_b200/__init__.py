@@ -522,7 +522,7 @@ class KV4Cache:
 
     k_pages, v_pages: uint8 CUDA tensors [num_pages, kv_heads, page_size * 9 * head_dim / 16], contiguous (KV4Cache.empty
     makes them).  k_scale, v_scale: the static fp32 factors of all values, amax / 2688 of a calibration set for the
-    formats' whole range."""
+    formats' whole range.  None of them can be changed afterwards."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_size: int, head_dim: int = 128,
                  k_scale: float = 1.0, v_scale: float = 1.0):
@@ -539,7 +539,13 @@ class KV4Cache:
         self.device, self._dev = k_pages.device, k_pages.get_device()
         self._struct = _CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), self.num_pages, self.page_size,
                                     self.kv_heads, self.head_dim, self.k_scale, self.v_scale)
-        self._ref, self._at = ctypes.byref(self._struct), ctypes.addressof(self._struct)
+        self._ref = ctypes.byref(self._struct)
+        self._at = ctypes.addressof(self._struct)
+
+    def __setattr__(self, name, value):              # the calls read what __init__ laid down for them
+        if "_at" in self.__dict__:
+            raise AttributeError(f"KV4Cache.{name} cannot be changed: make another cache over the same pages")
+        super().__setattr__(name, value)
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int = 64, head_dim: int = 128, k_scale: float = 1.0,

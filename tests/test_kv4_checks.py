@@ -273,6 +273,15 @@ def test_binding_cache(lib):
         fq.KV4Cache(S((5, 2, 32 * 64), U8), S((5, 2, 32 * 64), U8), 32, 128)
 
 
+@pytest.mark.parametrize("name", ["k_scale", "v_scale", "k_pages", "v_pages", "page_size", "head_dim", "num_pages"])
+def test_a_cache_does_not_change_behind_its_calls(lib, name):
+    cache = a_cache()
+    was = getattr(cache, name)
+    with pytest.raises(AttributeError, match=name):
+        setattr(cache, name, was)
+    assert getattr(cache, name) is was
+
+
 def test_binding_rope(lib):
     base = dict(x=S((6, 4, 128), BF), positions=S((6,), I64), freq=S((64,), F64), out=S((6, 4, 128), BF))
     call = lambda **kw: fq.fp8q_rope(**{**base, **kw})  # noqa: E731
