@@ -18,8 +18,8 @@
 // item as soon as the last S of the item before is done, ahead of that item's
 // end.  Tensor memory (512 columns): S0, S1 (P over the first half of S), O0,
 // O1.  The list of (256 rows, key head) items, each with its own run of 128-key
-// steps, is cut over the CTAs as in the kernel for few rows; parts of a cut item
-// are joined by the last of its CTAs, in CTA order.
+// steps, is cut over the CTAs as in the kernel for few rows, or each item by
+// itself; its parts are joined by the last of its CTAs, in CTA order.
 //
 // Measured: 2048 new tokens of 32 heads behind 6144 cached ones (8 key heads, D =
 // 128): 240 us, 1.0 PFLOP/s of the visible products (0.61 of what a library
@@ -86,9 +86,10 @@ constexpr int kOver = 2;
 
 // A part joined costs about 3 us (the parts of an item are read by its last CTA alone), a step 2 us once the pipeline
 // is full: where there are few steps a CTA takes at least kLeast of them (256 rows of 8 heads over 2000 keys: 54 -> 35
-// us, over 4096: 67 -> 51), and where there are few items each is left to one CTA whose steps take at most kJoinCost
-// longer than an even share (256 rows over 500 keys: 27 -> 22 us, 2000 rows over 2000: 53 -> 47).
-constexpr int kLeast = 4, kJoinCost = 12;
+// us; with 2 or 6, 40).  And where there are no more items than CTAs, each is cut by itself, into equal parts, unless
+// that takes kJoinCost steps longer than an even share of the list, which gives most CTAs the ends of two items (256
+// rows over 500 keys: 27 -> 22 us, over 8000: 88 -> 63; 2000 rows over 2000: 53 -> 42; at 0 the list again).
+constexpr int kLeast = 4, kJoinCost = 6;
 
 struct Job {
   Unit x;
@@ -284,10 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   Range range;
   range.q = quotient(total, ctas);
   range.r = total - range.q * ctas;
-  const bool by_item = items <= static_cast<int>(gridDim.x) && longest + kOver <= range.q + kJoinCost;
-  if (static_cast<int>(blockIdx.x) >= (by_item ? items : ctas)) return;
-  const int64_t begin = by_item ? static_cast<int64_t>(blockIdx.x) : range.begin(blockIdx.x);
-  const int64_t end = by_item ? begin + 1 : range.begin(blockIdx.x + 1);
+  // Where there are no more items than CTAs each may be left to `each` CTAs of its own, in parts of equal steps.
+  const int each = items > 0 ? max(1, min(static_cast<int>(gridDim.x) / items, longest / kLeast)) : 1;
+  const bool apart = items <= static_cast<int>(gridDim.x) && (longest + each - 1) / each + kOver <= range.q + kJoinCost;
+  if (static_cast<int>(blockIdx.x) >= (apart ? items * each : ctas)) return;
+  const int64_t begin = apart ? static_cast<int64_t>(blockIdx.x) / each : range.begin(blockIdx.x);
+  const int64_t end = apart ? begin + 1 : range.begin(blockIdx.x + 1);
   if (begin == end) return;
   if (warp == 12) {
     tmem_alloc(tmem_slot, 512);
@@ -296,16 +299,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   {
     int64_t ahead = 0;
     for (int base = 0; base < units; base += kThreads) {
-      const int64_t all = units <= kThreads ? everything : scan(base), all_w = by_item ? all >> 40 : all & (kOneItem - 1);
+      const int64_t all = units <= kThreads ? everything : scan(base), all_w = apart ? all >> 40 : all & (kOneItem - 1);
       if (begin >= ahead && begin < ahead + all_w) {
-        const int64_t at = begin - ahead - (by_item ? before >> 40 : before & (kOneItem - 1));
-        if (at >= 0 && at < (by_item ? mine >> 40 : mine & (kOneItem - 1))) {      // the first job is this thread's
+        const int64_t at = begin - ahead - (apart ? before >> 40 : before & (kOneItem - 1));
+        if (at >= 0 && at < (apart ? mine >> 40 : mine & (kOneItem - 1))) {      // the first job is this thread's
           const int u = base + static_cast<int>(threadIdx.x);
           const Unit x = unit_of(p, u);
-          const int steps = x.steps + kOver, head = static_cast<int>(by_item ? at : quotient(at, steps));
-          const int off = by_item ? kOver : static_cast<int>(at - static_cast<int64_t>(head) * steps);
-          make_job(x, u, head, max(0, off - kOver), begin + max(0, kOver - off), by_item ? begin + x.steps : end, jobs);
-          misc[18] = by_item ? begin + x.steps : end;
+          if (apart) {
+            const int parts = min(each, x.steps), k = min(static_cast<int>(blockIdx.x) % each, parts);
+            const int s0 = static_cast<int>(static_cast<int64_t>(x.steps) * k / parts);
+            const int s1 = static_cast<int>(static_cast<int64_t>(x.steps) * min(k + 1, parts) / parts);
+            make_job(x, u, static_cast<int>(at), s0, s0, s1, jobs);
+            misc[18] = s1;
+          } else {
+            const int steps = x.steps + kOver, head = static_cast<int>(quotient(at, steps));
+            const int off = static_cast<int>(at - static_cast<int64_t>(head) * steps);
+            make_job(x, u, head, max(0, off - kOver), begin + max(0, kOver - off), end, jobs);
+            misc[18] = end;
+          }
         }
         break;
       }
@@ -313,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
   }
   if (threadIdx.x == 0) {
-    misc[16] = range.q;
-    misc[17] = range.r;
+    misc[16] = apart ? -1 : range.q;
+    misc[17] = apart ? each : range.r;
   }
   tc_fence_before();
   __syncthreads();
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
   const bool none = jobs[0].steps <= 0;              // the range lies ahead of an item's first step
   // What a role needs between items only is read back from shared memory there, not held in registers.
-  const volatile int64_t* kept = misc;               // range.q, range.r, this CTA's end
+  const volatile int64_t* kept = misc;               // range.q and range.r (or -1 and `each`), this CTA's end
   auto range_end = [&]() { return kept[18]; };
 
   // counts of what a role has waited for, over all jobs
@@ -533,7 +544,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           tc_fence_before();
           __stcg(slot + kRows * D + row_in, top);
           __stcg(slot + kRows * (D + 1) + row_in, sum);
-          const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
+          int c0, parts;
+          if (range.q < 0) {                         // CTAs of its own
+            c0 = static_cast<int>(blockIdx.x) / static_cast<int>(range.r) * static_cast<int>(range.r);
+            parts = min(static_cast<int>(range.r), job.x.steps);
+          } else {
+            c0 = range.owner(i0);
+            parts = range.owner(i1 - 1) - c0 + 1;
+          }
           unsigned* count = p.count + c0 * 8 + warp;
           __threadfence();
           __syncwarp();

@@ -363,6 +363,10 @@ ATTENTIONS = [  # lens, rows, Hq, H, D, page, options
     ([513], [129], 8, 8, 128, 64, {}),
     ([700], [64], 12, 4, 64, 128, dict(q_kw=dict(wide=20, at=1))),      # queries inside fused rows
     ([180], [90], 5, 5, 128, 16, dict(q_kw=dict(head_major=True))),
+    ([300, 90], [3, 2], 16, 2, 128, 16, {}),                            # 24 rows, 25, 80 and 81: where the tiles change
+    ([300, 90], [5, 2], 25, 5, 64, 32, {}),
+    ([300, 90], [10, 3], 16, 2, 128, 64, dict(pad=1)),
+    ([300, 290], [27, 3], 6, 2, 64, 16, {}),
 ]
 
 
