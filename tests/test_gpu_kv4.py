@@ -15,6 +15,7 @@ Tolerances.
   a = sum of w |v|.  lse: d + 2^-11 (where the sum is of rounded weights) + n 2^-24, and 2^-23 |lse|.
 """
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -515,6 +516,42 @@ def test_attention_on_another_stream():
         got, _ = b.call()
     s.synchronize()
     assert torch.equal(want, got)
+
+
+def test_calls_at_once_from_two_threads_on_two_streams():
+    """Each with a workspace of its own: appends into one cache's different pages, attention of one token and of many."""
+    kinds = [Batch([1500, 700], [1, 1], 8, 2, 128, 64, seed=10), Batch([900, 333], [130, 70], 8, 2, 128, 64, seed=11)]
+    want = [b.call() for b in kinds]
+    shared = fq.KV4Cache.empty(20, 2, 64, 128, 0.004, 0.004)
+    k, v = heads(640, 2, 128, 1), heads(640, 2, 128, 2)
+    slots = torch.arange(1280, device=DEV).view(2, 640)
+    freq, positions = fq.fp8q_rope_frequencies(128), torch.arange(640, device=DEV)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        b, T = kinds[i], kinds[i].q.shape[0]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ws = torch.zeros(fq.fp8q_kv4_attention_workspace_size(b.cache, 2, T, 8, max(b.rows)), dtype=torch.uint8,
+                             device=DEV)
+            for _ in range(30):
+                fq.fp8q_kv4_append(shared, k, v, slots[i], positions, freq)
+                out, lse = b.call(workspace=ws)
+                torch.cuda.current_stream().synchronize()
+                if not (torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    got = fq.fp8q_kv4_read(shared, slots.view(-1))
+    alone = fq.KV4Cache.empty(20, 2, 64, 128, 0.004, 0.004)
+    for i in range(2):
+        fq.fp8q_kv4_append(alone, k, v, slots[i], positions, freq)
+    assert all(torch.equal(a, b) for a, b in zip(got, fq.fp8q_kv4_read(alone, slots.view(-1))))
 
 
 def test_attention_over_a_cache_past_four_gigabytes():
