@@ -75,7 +75,7 @@ fp8q_status check_rows(const void* p, int64_t t, int64_t h) {
 
 // What a call of these sizes launches: the kernel for few rows with 8 nt rows a
 // tile, or (nt = 0) the one for many; `ctas` CTAs; and the workspace: a header
-// of arrival counters, two per CTA, then two partial results per CTA.
+// of arrival counters, then two partial results per CTA.
 constexpr size_t kWorkspaceHeader = 2 * fp8q::kv4::kMaxCtas * sizeof(unsigned);
 static_assert(kWorkspaceHeader == FP8Q_KV4_WORKSPACE_HEADER, "as declared");
 
@@ -95,7 +95,7 @@ AttentionPlan attention_plan(const fp8q_kv4_cache* c, int64_t T, int64_t Hq, int
   // against 88, 31 against 44, 200 against 194 us; 96 rows: 96 against 88, 34 against 44, 239 against 193.
   a.nt = rows <= 24 ? 1 : (rows <= 80 ? 2 : 0);
   a.ctas = sms * (a.nt == 1 ? (c->head_dim == 64 ? 5 : 4) : (a.nt == 2 ? 3 : 1));
-  const int most = fp8q::kv4::kMaxCtas;              // of whose counters each CTA has two
+  const int most = fp8q::kv4::kMaxCtas / (a.nt ? 1 : 4);       // a CTA has two of the header's counters, or eight
   if (a.ctas > most) a.ctas = most;
   const int64_t tile = a.nt ? 8 * a.nt : fp8q::kv4::many::kRows;
   a.row_tiles = static_cast<int>((rows + tile - 1) / tile);
