@@ -17,7 +17,7 @@ SOURCES = ["fp8q.cu", "kv4.cu"]
 PARTS = {
     "fp8q.cu": ["fp8q.cu", "ptx.cuh", "quant.cuh", "gemm_prefill.cuh", "gemm_decode.cuh", "gemv_w8a16.cuh",
                 "calib.cuh", "sched.cuh", "host.cuh"],
-    "kv4.cu": ["kv4.cu", "ptx.cuh", "rope.cuh", "kv4.cuh", "kv4_attention.cuh", "kv4_prefill.cuh", "host.cuh"],
+    "kv4.cu": ["kv4.cu", "ptx.cuh", "rope.cuh", "kv4.cuh", "kv4_list.cuh", "kv4_attention.cuh", "kv4_prefill.cuh", "host.cuh"],
 }
 DEPS = sorted({d for parts in PARTS.values() for d in parts})
 

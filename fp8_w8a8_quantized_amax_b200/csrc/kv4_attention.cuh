@@ -8,6 +8,7 @@
 #pragma once
 
 #include "kv4.cuh"
+#include "kv4_list.cuh"
 
 namespace fp8q {
 namespace kv4 {
@@ -30,7 +31,6 @@ struct AttnParams {
 };
 
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr int kMaxCtas = 1024;  // counters of each level in the workspace's header
 
 // The rows [r0, r0 + n) and cached tokens of sequence b, bounded to what the
 // tensors hold (a length that has to be cut sets the error word).
@@ -60,20 +60,6 @@ __device__ __forceinline__ int visible_first(const AttnParams& p, int pos) {
 __device__ __forceinline__ int visible_last(const AttnParams& p, const Seq& s, int pos) {
   return p.causal ? max(0, min(s.kv, pos + 1)) : s.kv;
 }
-
-// The list of all steps of a call, cut evenly over the CTAs.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {     // a >= 0, b > 0; mostly 32-bit values
-  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
-}
-
-struct Range {
-  int64_t q, r;   // CTA c takes q + 1 steps when c < r, else q
-  __device__ int64_t begin(int64_t c) const { return c * q + min(c, r); }
-  __device__ int owner(int64_t s) const {
-    const int64_t big = r * (q + 1);
-    return static_cast<int>(s < big ? quotient(s, q + 1) : r + quotient(s - big, q));
-  }
-};
 
 // A sum over the list holds its steps in the low 40 bits and its items above (the host bounds both).
 constexpr int64_t kOneItem = static_cast<int64_t>(1) << 40;
@@ -188,8 +174,6 @@ namespace few {
 
 constexpr int kTile = 32;     // keys of a warp per step
 constexpr int kStages = 2;
-constexpr int kJoin = 16;     // parts of an item joined at a time
-constexpr int kOver = 3;      // steps that an item costs beside its keys
 constexpr int kJoinCost = 4;  // steps that joining an item's parts takes (2: 500 keys 8.8 -> 10.1 us; 8: as 4)
 
 template <int D, int NT, int WARPS>
@@ -772,15 +756,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
       // parts (a long context of few heads) are joined in two levels: groups of consecutive CTAs first, each by its
       // last, into its first part's place, then the groups (92 parts of 4 KB by one CTA took 10 us, bound by what one SM
       // reads from L2).
-      const int c0 = range.owner(i0), parts = range.owner(i1 - 1) - c0 + 1;
-      const int width = parts <= kJoin ? parts : kJoin;          // parts a group
-      const int groups = (parts + width - 1) / width;
+      const int c0 = range.owner(i0);
+      const Joins joins = {c0, range.owner(i1 - 1) - c0 + 1};
       float* at0 = p.part + (2 * static_cast<int64_t>(c0) + 1) * L::kPart;
       float* at1 = p.part + 2 * (static_cast<int64_t>(c0) + 1) * L::kPart;     // the others', 2 kPart apart
       auto part_at = [&](int c) { return c == 0 ? at0 : at1 + 2 * static_cast<int64_t>(c - 1) * L::kPart; };
-      int from = (static_cast<int>(blockIdx.x) - c0) / width * width, n = min(width, parts - from), stride = 1;
-      unsigned* count = p.count + c0 + from;         // of the group: its first CTA's (an item that goes on past its end: one)
+      Meeting meet = joins.first(static_cast<int>(blockIdx.x));
       for (;;) {
+        const int from = meet.from, n = meet.n, stride = meet.stride;
+        unsigned* count = p.count + meet.counter;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) misc[10] = atom_add_acq_rel_gpu(count, 1u);
@@ -788,7 +772,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
         if (static_cast<int>(misc[10]) != n - 1) break;
         __threadfence();
         if (threadIdx.x == 0) *count = 0;
-        const bool final = stride > 1 || groups == 1;
         // the parts' bases and sums, over the warps' free stages
         auto mls = [&](int c) { return red_of(c % WARPS, stage) + c / WARPS * 2 * kRows; };
         for (int i = threadIdx.x; i < n * kRows; i += L::kThreads) {
@@ -810,7 +793,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
             sum += ml2.y * f;
             v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
           }
-          if (final) {
+          if (meet.final) {
             finish(r, d, v, top, sum);
           } else {
             float* dst = part_at(from);
@@ -821,11 +804,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
             }
           }
         }
-        if (final) break;
-        from = 0;
-        n = groups;
-        stride = width;
-        count = p.count + kMaxCtas + c0;
+        if (meet.final) break;
+        meet = joins.second();
         __syncthreads();                            // misc and mls are free again
       }
     }

@@ -1,0 +1,86 @@
+"""Attention over the 4-bit KV cache at long contexts and few parts too many, against 64-bit sums on the device."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_w8a8_quantized_amax_b200 as fq
+from tests import _kv4 as O
+from tests.test_gpu_kv4 import DEV, Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from fp8_w8a8_quantized_amax_b200 import build
+    build.build()
+    fq.device_error(clear=True)
+    yield
+    assert fq.device_error(clear=True) == 0
+
+
+def cached(pages, page, g, row, n, h):
+    """float64 [n, D] on the device: head h of the first n tokens of the pages in `row`."""
+    D = pages.shape[2] * 16 // 9 // page
+    codes, scales = O.views(pages[row.long()[:(n + page - 1) // page], h:h + 1], page, D)
+    codes, scales = codes.reshape(-1, D // 2)[:n].long(), scales.reshape(-1, D // 16)[:n].long()
+    e2m1 = torch.tensor(np.concatenate([O.E2M1, -O.E2M1]), device=DEV)
+    e4m3 = torch.tensor(np.concatenate([O.E4M3, [math.nan]]), device=DEV)
+    v = torch.stack([e2m1[codes & 15], e2m1[codes >> 4]], -1).reshape(n, D // 16, 16) * e4m3[scales][..., None]
+    return v.reshape(n, D) * float(np.float32(g))
+
+
+def attention(b, i, sm=None):
+    """What tests._kv4.attention gives for sequence i of a causal batch, as float64 tensors on the device; and max |v|."""
+    n, m, D, H = b.lens[i], b.rows[i], b.D, b.H
+    r0 = sum(b.rows[:i])
+    q = b.q[r0:r0 + m].double()
+    G = q.shape[1] // H
+    sm = float(np.float32(D ** -0.5 if sm is None else sm))
+    hide = torch.arange(n, device=DEV)[None] > torch.arange(n - m, n, device=DEV)[:, None]
+    o, a, big = torch.empty_like(q), torch.empty_like(q), 0.0
+    lse, e = (torch.empty(q.shape[:2], dtype=torch.float64, device=DEV) for _ in range(2))
+    for h in range(H):
+        k = cached(b.cache.k_pages, b.page, b.cache.k_scale, b.table_dev[i], n, h)
+        v = cached(b.cache.v_pages, b.page, b.cache.v_scale, b.table_dev[i], n, h)
+        big = max(big, float(v.abs().max()))
+        for x in range(h * G, (h + 1) * G):
+            s = (q[:, x] @ k.T * sm).masked_fill_(hide, -math.inf)
+            lse[:, x] = torch.logsumexp(s, -1)
+            w = torch.exp(s - lse[:, x, None])
+            o[:, x], a[:, x] = w @ v, w @ v.abs()
+            e[:, x] = (q[:, x].abs() @ k.abs().T * sm).masked_fill_(hide, 0.0).amax(-1)
+    return o, lse, a, e, big
+
+
+def check(b, i, out, lse, sm=None):
+    """Sequence i's rows of a call within the bounds that tests/test_gpu_kv4.py derives."""
+    n, r0 = b.lens[i], sum(b.rows[:i])
+    o, l, a, e, big = attention(b, i, sm)
+    out, lse = (x[r0:r0 + b.rows[i]].double() for x in (out, lse))
+    d = 2 * (b.D + 4) * 2.0 ** -24 * e
+    tol = 2 * (d[..., None] + 2.0 ** -20 + 2.0 ** -11 + n * 2.0 ** -24) * a + n * 2.0 ** -24 * big + 2.0 ** -8 * o.abs()
+    err = (out - o).abs()
+    assert bool((err <= tol).all()), f"sequence {i}: worst excess {float((err - tol).max()):.3g}"
+    assert bool(((lse - l).abs() <= d + 2.0 ** -11 + n * 2.0 ** -24 + 2.0 ** -23 * l.abs()).all()), f"sequence {i}: lse"
+
+
+@pytest.mark.parametrize("lens,H,Hq,D", [
+    ([91885, 182], 8, 8, 128), ([32000, 1000, 16384, 100000], 8, 32, 128), ([65536, 1000, 16000, 65536], 8, 32, 128),
+    ([16384] * 4, 8, 8, 128), ([131072] * 5, 7, 7, 128), ([700, 33000, 12000, 2500, 21000, 500, 30000, 9000], 8, 16, 64)])
+def test_items_whose_parts_leave_one_over_beside_other_items(lens, H, Hq, D):
+    """Items of 17, 33, ... parts, the last of them in a CTA that begins with the next item: every row is written, the
+    same in every call on one workspace, whose header is left zero."""
+    b = Batch(lens, [1] * len(lens), Hq, H, D, 64, seed=21)
+    need = fq.fp8q_kv4_attention_workspace_size(b.cache, len(lens), len(lens), Hq)
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    first = b.call(workspace=ws)
+    assert int(ws[:8192].count_nonzero()) == 0
+    for _ in range(30):
+        again = b.call(workspace=ws)
+        assert int(ws[:8192].count_nonzero()) == 0
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    for i in range(len(lens)):
+        check(b, i, *first)
