@@ -64,8 +64,19 @@ __device__ __forceinline__ int visible_last(const AttnParams& p, const Seq& s, i
 // A sum over the list holds its steps in the low 40 bits and its items above (the host bounds both).
 constexpr int64_t kOneItem = static_cast<int64_t>(1) << 40;
 
-// The softmax base is raised only when a score passes it by 2^kSlack: P, at most 256, keeps its precision in f16.
-constexpr float kSlack = 8.0f;
+// The softmax base.  It is raised only when a score passes the one before by 2^kSlack, and lies 2^kLift below the score
+// that raised it: the largest P of a row lies between 2^kLift and 2^(kLift + kSlack) = 2^15, the last power of two that
+// f16 has.  P is rounded to f16, the sum of the weights takes it unrounded; with kLift = 0 keys 16.5 nats below a
+// dominant one were off by 13%, and from 17.4 on nothing was left of them.  Now a weight keeps f16's 11 bits down to
+// 2^-21 of the row's largest, and n keys lose at most n 2^-32 of it below that.  Both are rounded so that P never passes
+// 2^15, whatever the size of the scores.
+constexpr float kSlack = 8.0f, kLift = 7.0f;
+// The negated base that a largest score asks for; infinity where it is minus infinity (no visible key).
+__device__ __forceinline__ float base_above(float top, float qscale) { return __fmaf_rd(-top, qscale, kLift); }
+// The score up to which it is kept.
+__device__ __forceinline__ float base_limit(float nbase, float qscale) {
+  return __fdiv_rd(__fsub_rd(kLift + kSlack, nbase), qscale);
+}
 
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -152,8 +163,9 @@ __device__ __forceinline__ float pow2(int k) { return __uint_as_float(static_cas
 // V^T's operand pairs two keys in a register: the two keys' nibbles are merged
 // into bytes (two logic operations for four values) before they are widened.
 // E2M1 times E4M3 is exact in f16.  Q is scaled by a power of two per row so
-// that its bf16 values are f16 values (all of them that are not below 2^-38 of
-// the row's largest); P, at most 2^kSlack, is rounded to f16.
+// that its bf16 values are f16 values (down to about 2^-31 of the row's largest;
+// below, they are rounded to multiples of 2^-38 of it at least); P is rounded to
+// f16.
 //
 // The keys of a (sequence, key head) are cut into steps of WARPS * 32; the
 // list of all steps is cut evenly over the CTAs (stream-K, as in the linear's
@@ -390,7 +402,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
                       ((key + scale_key) & in_page) * (D / 16));
   };
 
-  // per row: the scores' factor, the base m (negated; 0 before the first key), the score at which it is raised, the sum
+  // per row: the scores' factor, the base (negated; 0 before the first key), the score at which it is raised, the sum
   float qscale[NT][2], nbase[NT][2], limit[NT][2], l[NT][2];
   float o[kSteps][NT][4];
   auto stored_range = [&]() {
@@ -573,8 +585,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
             }
         }
       }
-      // Softmax over the tile: element i of sc is key (g, g + 8)[i / 2], row 2t + i % 2.  The base m is raised only
-      // when a score passes it by 2^8 (P, at most 256, keeps its precision in f16, and a sum of fp32 its own).
+      // Softmax over the tile: element i of sc is key (g, g + 8)[i / 2], row 2t + i % 2.
       if (__builtin_expect(!whole, 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -606,12 +617,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
           for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], d));
-            const float was = limit[nt][i] == -INFINITY ? -INFINITY : -nbase[nt][i];
-            const float now = fmaxf(was, top[i] * qscale[nt][i]);
-            if (now > was) {                        // (a row without a visible key so far stays at -infinity)
-              const float f = ex2(was - now);       // 0 from -infinity
-              nbase[nt][i] = -now;
-              limit[nt][i] = (now + kSlack) / qscale[nt][i];
+            // (a row without a visible key so far stays at a base of 0, and its limit at -infinity)
+            const float was = limit[nt][i] == -INFINITY ? INFINITY : nbase[nt][i];
+            const float now = base_above(top[i], qscale[nt][i]);
+            if (now < was) {
+              const float f = ex2(now - was);       // 0 from infinity
+              nbase[nt][i] = now;
+              limit[nt][i] = base_limit(now, qscale[nt][i]);
               l[nt][i] *= f;
 #pragma unroll
               for (int d = 0; d < kSteps; ++d) {

@@ -461,12 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           if (!__all_sync(0xFFFFFFFFu, first <= 0 && last >= kKeys)) row_mask(ts, first, last);
           const float top = row_max(ts);
           if (__any_sync(0xFFFFFFFFu, top > limit)) {
-            const float was = limit == -INFINITY ? -INFINITY : -nbase, now = fmaxf(was, top * qscale);
+            const float was = limit == -INFINITY ? INFINITY : nbase, now = base_above(top, qscale);
             float f = 1.0f;
-            if (now > was) {
-              f = ex2(was - now);                    // 0 from -infinity
-              nbase = -now;
-              limit = (now + kSlack) / qscale;
+            if (now < was) {
+              f = ex2(now - was);                    // 0 from infinity
+              nbase = now;
+              limit = base_limit(now, qscale);
               sum *= f;
             }
             if (j > 0) {                             // S of this step was issued after O's last product: O is at rest

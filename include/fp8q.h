@@ -441,6 +441,9 @@ FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* s
  *   q_start         [B + 1] int32, ascending, q_start[B] <= T; NULL for one row
  *                   per sequence (row b is sequence b's; then max_q_len is 1).
  *   sm_scale        > 0, finite, as is its product with k_scale (1 / sqrt(D) for most models).
+ *                   Scores sm_scale q.k are to stay below 2^27 in magnitude (they are fp32, which
+ *                   holds no fractions there).  Weights are rounded to f16 with the row's
+ *                   largest at 2^7 .. 2^15: one below 2^-21 of it keeps fewer than 11 bits.
  *   max_q_len       the largest number of rows of a sequence; longer ones set the
  *                   device error word.  Lengths stay on the device: a captured call
  *                   can be replayed with other lengths up to these bounds.

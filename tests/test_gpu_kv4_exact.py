@@ -56,12 +56,13 @@ def attention(b, i, sm=None):
 
 
 def check(b, i, out, lse, sm=None):
-    """Sequence i's rows of a call within the bounds that tests/test_gpu_kv4.py derives."""
+    """Sequence i's rows of a call within the bounds that tests/test_gpu_kv4.py derives, but for what small weights lose
+    in f16 (n 2^-32 of max|v|, see below)."""
     n, r0 = b.lens[i], sum(b.rows[:i])
     o, l, a, e, big = attention(b, i, sm)
     out, lse = (x[r0:r0 + b.rows[i]].double() for x in (out, lse))
     d = 2 * (b.D + 4) * 2.0 ** -24 * e
-    tol = 2 * (d[..., None] + 2.0 ** -20 + 2.0 ** -11 + n * 2.0 ** -24) * a + n * 2.0 ** -24 * big + 2.0 ** -8 * o.abs()
+    tol = 2 * (d[..., None] + 2.0 ** -20 + 2.0 ** -11 + n * 2.0 ** -24) * a + n * 2.0 ** -32 * big + 2.0 ** -8 * o.abs()
     err = (out - o).abs()
     assert bool((err <= tol).all()), f"sequence {i}: worst excess {float((err - tol).max()):.3g}"
     assert bool(((lse - l).abs() <= d + 2.0 ** -11 + n * 2.0 ** -24 + 2.0 ** -23 * l.abs()).all()), f"sequence {i}: lse"
@@ -84,3 +85,60 @@ def test_items_whose_parts_leave_one_over_beside_other_items(lens, H, Hq, D):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     for i in range(len(lens)):
         check(b, i, *first)
+
+
+@pytest.mark.parametrize("rows,Hq,H,D", [(1, 8, 2, 128), (1, 6, 2, 64), (8, 4, 1, 128), (8, 4, 1, 64), (90, 2, 2, 128), (70, 4, 1, 64)])
+@pytest.mark.parametrize("gap", [9.0, 14.0, 16.5, 17.0, 17.4, 18.5])
+def test_many_small_weights_beside_dominant_ones(rows, Hq, H, D, gap):
+    """One key in 32 dominates and has values of zero; what comes out is the others', e^-gap and less each.
+
+    A weight is rounded to f16, 2^-11 of itself or, where that has no more bits, 2^-25 of the unit, which is at most 2^-7 of
+    the row's largest weight (2^0 by 2^7 at the least).  So n keys lose at most n 2^-32 of the largest weight times max|v|,
+    and the sum they are divided by is S = sum exp(s - max s) times that weight.  The other terms are those of
+    tests/test_gpu_kv4.py, whose n 2^-24 max|v| this one replaces."""
+    n = 700
+    b = Batch([n], [rows], Hq, H, D, 64, seed=31, kg=2.0 ** -8, vg=2.0 ** -8)
+    j = torch.arange(n)
+    slots = (b.table[0].long()[j // 64] * 64 + j % 64).to(DEV)
+    g = torch.Generator().manual_seed(5)
+    sink = (j % 32 == 3).view(-1, 1, 1)
+    # 0.75 = 6 * 32 * 2^-8 is a value of the cache; v has one sign, so that nothing cancels
+    k = torch.where(sink, 0.75, 0.0).expand(n, H, D).to(torch.bfloat16).contiguous().to(DEV)
+    v = torch.where(sink, 0.0, torch.randn((n, H, D), generator=g).abs()).to(torch.bfloat16).to(DEV)
+    fq.fp8q_kv4_append(b.cache, k, v, slots)
+    # rows of smaller and smaller gaps: 1 - r / 256 is a bf16
+    b.q.copy_((1.0 - torch.arange(rows, device=DEV) / 256.0).view(-1, 1, 1).expand_as(b.q))
+    sm = float(np.float32(gap / (0.75 * D)))
+    out, lse = b.call(sm_scale=sm)
+    o, l, a, e, big = attention(b, 0, sm)
+    d = 2 * (D + 4) * 2.0 ** -24 * e
+    S = torch.exp(l - e)                             # (a row's largest score is e: the products have one sign)
+    tol = 2 * (d[..., None] + 2.0 ** -20 + 2.0 ** -11 + n * 2.0 ** -24) * a + n * 2.0 ** -32 * big / S[..., None] + 2.0 ** -8 * o
+    err = (out.double() - o).abs()
+    assert bool((err <= tol).all()), f"off by {float((err / o).max()):.3g} of itself, allowed {float((tol / o).max()):.3g}"
+    assert bool(((lse.double() - l).abs() <= d + 2.0 ** -11 + n * 2.0 ** -24 + 2.0 ** -23 * l.abs()).all())
+
+
+@pytest.mark.parametrize("rows,Hq,H,D", [(1, 8, 2, 128), (8, 4, 1, 64), (90, 2, 2, 128), (70, 4, 1, 64)])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 24, 2.0 ** 26])
+def test_scores_of_any_size_below_the_limit_give_numbers(rows, Hq, H, D, size):
+    """One key's score is +-size and the others' a part of it: where the gap to the next is above the bound of the scores'
+    own error, the output is that key's value (or that of the keys of equal score), to f16's and bf16's half steps."""
+    n = 300
+    b = Batch([n], [rows], Hq, H, D, 64, seed=33, kg=2.0 ** -8, vg=2.0 ** -8)
+    j = torch.arange(n)
+    slots = (b.table[0].long()[j // 64] * 64 + j % 64).to(DEV)
+    # scores size * (1, 1/2, 1/4, ...) over and over, and zero: powers of two are values of the cache
+    k = (0.75 * 2.0 ** -(j % 5).float()).view(-1, 1, 1).expand(n, H, D).to(torch.bfloat16).contiguous().to(DEV)
+    v = torch.randn((n, H, D), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(DEV)
+    fq.fp8q_kv4_append(b.cache, k, v, slots)
+    for sign in (1.0, -1.0):
+        b.q.copy_((sign * (1.0 - torch.arange(rows, device=DEV) / 256.0)).view(-1, 1, 1).expand_as(b.q))
+        sm = float(np.float32(size / (0.75 * D)))
+        out, lse = b.call(sm_scale=sm)
+        o, l, a, e, big = attention(b, 0, sm)
+        # equal keys have equal scores, so only the largest score's keys are left, with equal weights; sums of up to n
+        tol = 2 * (2.0 ** -11 + n * 2.0 ** -24) * a + 2.0 ** -8 * o.abs()
+        assert bool(((out.double() - o).abs() <= tol).all())
+        d = 2 * (D + 4) * 2.0 ** -24 * e
+        assert bool(((lse.double() - l).abs() <= d + 2.0 ** -11 + n * 2.0 ** -24 + 2.0 ** -23 * l.abs()).all())
