@@ -337,7 +337,8 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   if ((st = check_rows(Q_bf16, q_token_stride, q_head_stride)) != FP8Q_OK) return st;
   if ((st = check_rows(O_bf16, o_token_stride, o_head_stride)) != FP8Q_OK) return st;
   if (rows_overlap(T, Hq, cache->head_dim, o_token_stride, o_head_stride)) return FP8Q_ERR_INVALID_ARG;
-  if (!page_table || !kv_len || (B > 1 && table_stride < max_pages)) return FP8Q_ERR_INVALID_ARG;
+  // (a table without a page needs no memory: every sequence is empty)
+  if ((!page_table && max_pages > 0) || !kv_len || (B > 1 && table_stride < max_pages)) return FP8Q_ERR_INVALID_ARG;
   if (!workspace) return FP8Q_ERR_INVALID_ARG;   // its size needs the device; presence and alignment do not
   if (!aligned(page_table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(lse, 4) ||
       !aligned(workspace, 16))

@@ -436,7 +436,7 @@ FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* s
  *                   not overlap each other or Q.  Q's values must be finite.
  *   page_table      [B, max_pages] int32, row stride table_stride >= max_pages;
  *                   max_pages * page_size < 2^31 - 65536.  Entries that no visible
- *                   key needs are not read.
+ *                   key needs are not read; NULL where max_pages is 0.
  *   kv_len          [B] int32, 0 <= kv_len[b] <= max_pages * page_size.
  *   q_start         [B + 1] int32, ascending, q_start[B] <= T; NULL for one row
  *                   per sequence (row b is sequence b's; then max_q_len is 1).

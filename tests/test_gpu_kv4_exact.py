@@ -142,3 +142,17 @@ def test_scores_of_any_size_below_the_limit_give_numbers(rows, Hq, H, D, size):
         assert bool(((out.double() - o).abs() <= tol).all())
         d = 2 * (D + 4) * 2.0 ** -24 * e
         assert bool(((lse.double() - l).abs() <= d + 2.0 ** -11 + n * 2.0 ** -24 + 2.0 ** -23 * l.abs()).all())
+
+
+@pytest.mark.parametrize("rows,q_start", [(1, False), (3, True), (90, True)])
+def test_sequences_that_are_all_empty_need_no_page(rows, q_start):
+    cache = fq.KV4Cache.empty(2, 2, 16, 128)
+    q = torch.randn((2 * rows + 1, 8, 128), device=DEV).to(torch.bfloat16)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device=DEV)
+    start = torch.tensor([0, rows, 2 * rows], dtype=torch.int32, device=DEV) if q_start else None
+    table = torch.zeros((2, 0), dtype=torch.int32, device=DEV)
+    for ws in (None, torch.zeros(fq.fp8q_kv4_attention_workspace_size(cache, 2, q.shape[0], 8, rows), dtype=torch.uint8, device=DEV)):
+        fq.fp8q_kv4_attention(q, cache, table, torch.zeros(2, dtype=torch.int32, device=DEV), start, rows, out=out, lse=lse,
+                              workspace=ws)
+        assert bool((out[:-1] == 0).all()) and bool((out[-1] == 7.0).all())
+        assert bool((lse[:-1] == -math.inf).all()) and bool((lse[-1] == 7.0).all())

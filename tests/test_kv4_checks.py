@@ -399,3 +399,16 @@ def test_package_fails_loudly_without_the_cpp_binding(monkeypatch, L):
     monkeypatch.setattr(fq, "BINDING_PATH", "/nonexistent/_kv4_binding.so")
     with pytest.raises(ImportError):
         fq._Binding().rope
+
+
+# -------------------------------------------------------- empty page tables ---
+
+@no_gpu
+@pytest.mark.parametrize("kw,want", [
+    (dict(mp=0, ts=0, table=None), VALID), (dict(mp=0, ts=0), VALID), (dict(mp=0, ts=0, table=None, qs=None, mq=1), VALID),
+    (dict(mp=0, ts=0, table=None, kv=None), INV), (dict(mp=1, ts=1, table=None), INV), (dict(mp=0, ts=-1, table=None), INV),
+])
+def test_attention_over_sequences_without_pages(L, kw, want):
+    """A [B, 0] page table, as torch makes it for sequences that are all empty: no memory, and none is read."""
+    assert torch.zeros((3, 0), dtype=I32).data_ptr() == 0
+    assert attend(L, **kw) == want
