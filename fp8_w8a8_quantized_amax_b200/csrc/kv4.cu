@@ -18,12 +18,16 @@ int fp8q_kv4_error_word(int clear, int* word) {
 
 namespace {
 
-constexpr int64_t kStrideMax = static_cast<int64_t>(1) << 40;   // keeps every offset inside 63 bits
+constexpr int64_t kStrideMax = static_cast<int64_t>(1) << 40;
+constexpr int64_t kExtentMax = static_cast<int64_t>(1) << 48;   // elements; more than a device's memory has addresses for
 
 bool finite_positive(float v) { return v > 0.0f && v < 3.0e38f; }   // also rejects NaN
 
-// Strides of a [T, H, D] tensor with contiguous heads, in elements.
-bool bad_strides(int64_t t, int64_t h) { return t < 0 || h < 0 || t > kStrideMax || h > kStrideMax; }
+// Strides of a [T, H, D] tensor with contiguous heads, in elements (those of a dimension of size 1 do not matter): no
+// offset passes kExtentMax, so what is computed of them stays inside 63 bits.
+bool bad_strides(int64_t T, int64_t H, int64_t t, int64_t h) {
+  return t < 0 || h < 0 || (T > 1 && t > kExtentMax / (T - 1)) || (H > 1 && h > kExtentMax / (H - 1));
+}
 
 // Whether the (token, head) rows of a tensor that is written overlap.
 bool rows_overlap(int64_t T, int64_t H, int64_t D, int64_t t, int64_t h) {
@@ -67,8 +71,8 @@ fp8q::kv4::Cache device_cache(const fp8q_kv4_cache* c) {
 }
 
 // A bf16 [T, heads, D] operand of the cache's entry points.
-fp8q_status check_rows(const void* p, int64_t t, int64_t h) {
-  if (!p || bad_strides(t, h)) return FP8Q_ERR_INVALID_ARG;
+fp8q_status check_rows(const void* p, int64_t T, int64_t H, int64_t t, int64_t h) {
+  if (!p || bad_strides(T, H, t, h)) return FP8Q_ERR_INVALID_ARG;
   if (!aligned(p, 16) || t % 8 != 0 || h % 8 != 0) return FP8Q_ERR_MISALIGNED;
   return FP8Q_OK;
 }
@@ -189,7 +193,7 @@ fp8q_status fp8q_rope(const void* X_bf16, int64_t T, int64_t H, int64_t D, int64
   fp8q_status st = check_rope(positions, freq, rot_dim, D, flags, mscale);
   if (st != FP8Q_OK) return st;
   if (!X_bf16 || !Y_bf16) return FP8Q_ERR_INVALID_ARG;
-  if (bad_strides(x_token_stride, x_head_stride) || bad_strides(y_token_stride, y_head_stride))
+  if (bad_strides(T, H, x_token_stride, x_head_stride) || bad_strides(T, H, y_token_stride, y_head_stride))
     return FP8Q_ERR_INVALID_ARG;
   if (T > kInt32Max || H > 65536 || D > 65536 || T * H > kInt32Max) return FP8Q_ERR_UNSUPPORTED;
   if (rows_overlap(T, H, D, y_token_stride, y_head_stride)) return FP8Q_ERR_INVALID_ARG;
@@ -247,8 +251,8 @@ fp8q_status fp8q_kv4_append(const fp8q_kv4_cache* cache, const void* K_bf16, int
   if (st != FP8Q_OK) return st;
   if (T < 0) return FP8Q_ERR_INVALID_ARG;
   if (T == 0) return FP8Q_OK;
-  if ((st = check_rows(K_bf16, k_token_stride, k_head_stride)) != FP8Q_OK) return st;
-  if ((st = check_rows(V_bf16, v_token_stride, v_head_stride)) != FP8Q_OK) return st;
+  if ((st = check_rows(K_bf16, T, cache->kv_heads, k_token_stride, k_head_stride)) != FP8Q_OK) return st;
+  if ((st = check_rows(V_bf16, T, cache->kv_heads, v_token_stride, v_head_stride)) != FP8Q_OK) return st;
   if (!slots) return FP8Q_ERR_INVALID_ARG;
   if (!aligned(slots, 8)) return FP8Q_ERR_MISALIGNED;
   if (positions || freq) {
@@ -287,8 +291,8 @@ fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* slots, int
   if (st != FP8Q_OK) return st;
   if (T < 0) return FP8Q_ERR_INVALID_ARG;
   if (T == 0) return FP8Q_OK;
-  if ((st = check_rows(K_bf16, k_token_stride, k_head_stride)) != FP8Q_OK) return st;
-  if ((st = check_rows(V_bf16, v_token_stride, v_head_stride)) != FP8Q_OK) return st;
+  if ((st = check_rows(K_bf16, T, cache->kv_heads, k_token_stride, k_head_stride)) != FP8Q_OK) return st;
+  if ((st = check_rows(V_bf16, T, cache->kv_heads, v_token_stride, v_head_stride)) != FP8Q_OK) return st;
   if (rows_overlap(T, cache->kv_heads, cache->head_dim, k_token_stride, k_head_stride) ||
       rows_overlap(T, cache->kv_heads, cache->head_dim, v_token_stride, v_head_stride))
     return FP8Q_ERR_INVALID_ARG;
@@ -334,8 +338,8 @@ fp8q_status fp8q_kv4_attention(const fp8q_kv4_cache* cache, const void* Q_bf16, 
   if (!finite_positive(sm_scale) || !(sm_scale * cache->k_scale < 1.0e38f)) return FP8Q_ERR_INVALID_ARG;
   if (T == 0 || B == 0) return FP8Q_OK;
   if (!q_start && (T < B || max_q_len != 1)) return FP8Q_ERR_INVALID_ARG;
-  if ((st = check_rows(Q_bf16, q_token_stride, q_head_stride)) != FP8Q_OK) return st;
-  if ((st = check_rows(O_bf16, o_token_stride, o_head_stride)) != FP8Q_OK) return st;
+  if ((st = check_rows(Q_bf16, T, Hq, q_token_stride, q_head_stride)) != FP8Q_OK) return st;
+  if ((st = check_rows(O_bf16, T, Hq, o_token_stride, o_head_stride)) != FP8Q_OK) return st;
   if (rows_overlap(T, Hq, cache->head_dim, o_token_stride, o_head_stride)) return FP8Q_ERR_INVALID_ARG;
   // (a table without a page needs no memory: every sequence is empty)
   if ((!page_table && max_pages > 0) || !kv_len || (B > 1 && table_stride < max_pages)) return FP8Q_ERR_INVALID_ARG;

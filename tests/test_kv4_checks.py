@@ -412,3 +412,24 @@ def test_attention_over_sequences_without_pages(L, kw, want):
     """A [B, 0] page table, as torch makes it for sequences that are all empty: no memory, and none is read."""
     assert torch.zeros((3, 0), dtype=I32).data_ptr() == 0
     assert attend(L, **kw) == want
+
+
+# --------------------------------------------------- strides of any product ---
+
+FAR = 1 << 40           # a stride; with 2^23 + 1 tokens the last one's offset is 2^63
+
+
+@no_gpu
+@pytest.mark.parametrize("T,t,h,want", [
+    ((1 << 23) + 1, FAR, FAR, INV),                 # token 1 of head 0 is token 0 of head 1, past what 63 bits can tell
+    ((1 << 8) + 1, FAR, 128, VALID), ((1 << 8) + 2, FAR, 128, INV),     # up to an offset of 2^48 elements
+    (2, 1 << 48, 128, VALID), (2, (1 << 48) + 8, 128, INV), (2, (1 << 62), 128, INV),
+    (1, (1 << 62), 128, VALID),                     # one token has no token stride
+])
+def test_offsets_stay_inside_63_bits(L, T, t, h, want):
+    c = cache(kv_heads=2)
+    assert rope(L, T=T, H=2, xt=0, xh=0, yt=t, yh=h) == want
+    assert rope(L, T=T, H=2, xt=t, xh=h, yt=256, yh=128) == want
+    assert append(L, c, T=T, kt=t, kh=h, vt=256) == want and append(L, c, T=T, vt=t, vh=h, kt=256) == want
+    assert read(L, c, T=T, kt=t, kh=h, vt=256) == want and read(L, c, T=T, vt=t, vh=h, kt=256) == want
+    assert attend(L, c, T=T, Hq=2, ot=t, oh=h, qt=0) == want and attend(L, c, T=T, Hq=2, qt=t, qh=h, ot=256) == want
