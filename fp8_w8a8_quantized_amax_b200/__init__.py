@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 from typing import Optional, Tuple
 
@@ -472,6 +473,14 @@ def _list(t: torch.Tensor, name: str, dtype, numel: int, dev: int) -> int:
     return t.data_ptr()
 
 
+def _whole(n, name: str) -> int:
+    """A whole number (numpy's too) that a C int64 holds: ctypes would drop the bits above."""
+    n = operator.index(n)
+    if not -2 ** 63 <= n < 2 ** 63:
+        raise ValueError(f"{name} must fit in 64 bits, got {n}")
+    return n
+
+
 def fp8q_rope_frequencies(rot_dim: int, theta: float = 500000.0, scaling: Optional[dict] = None,
                           device="cuda") -> torch.Tensor:
     """The rot_dim / 2 rotary frequencies (fp64, radians per position) on `device`.
@@ -507,14 +516,15 @@ def fp8q_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, inte
     pairs = freq.numel()
     at, f = _list(positions, "positions", torch.int64, T, dev), _list(freq, "freq", torch.float64, pairs, dev)
     yt, yh = (xt, xh) if out is x else _heads(out, "out", dev, shape)
-    _call(dev, "fp8q_rope", x.data_ptr(), T, H, D, xt, xh, at, f, 2 * pairs, flags, mscale, out.data_ptr(),
+    _call(dev, "fp8q_rope", x.data_ptr(), T, H, D, xt, xh, at, f, 2 * pairs, flags, float(mscale), out.data_ptr(),
           yt, yh)
     return out
 
 
 def fp8q_kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
     """Bytes of one page of a KV4Cache's k_pages (or v_pages); 0 for sizes that are not supported."""
-    return int(lib().fp8q_kv4_page_bytes(page_size, kv_heads, head_dim))
+    return int(lib().fp8q_kv4_page_bytes(_whole(page_size, "page_size"), _whole(kv_heads, "kv_heads"),
+                                         _whole(head_dim, "head_dim")))
 
 
 class KV4Cache:
@@ -576,7 +586,7 @@ def fp8q_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: to
     elif positions is not None or freq is not None:
         raise ValueError("positions and freq are given together")
     _call(dev, "fp8q_kv4_append", cache._ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-          _list(slots, "slots", torch.int64, T, dev), T, at, f, R, flags, mscale)
+          _list(slots, "slots", torch.int64, T, dev), T, at, f, R, flags, float(mscale))
 
 
 def fp8q_kv4_read(cache: KV4Cache, slots: torch.Tensor, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
@@ -595,8 +605,9 @@ def fp8q_kv4_read(cache: KV4Cache, slots: torch.Tensor, out: Optional[Tuple[torc
 
 def fp8q_kv4_attention_workspace_size(cache: KV4Cache, num_seqs: int, tokens: int, q_heads: int,
                                       max_q_len: int = 1) -> int:
+    sizes = (_whole(num_seqs, "num_seqs"), _whole(tokens, "tokens"), _whole(q_heads, "q_heads"), _whole(max_q_len, "max_q_len"))
     with torch.cuda.device(cache._dev):
-        return int(lib().fp8q_kv4_attention_workspace_size(cache._ref, num_seqs, tokens, q_heads, max_q_len))
+        return int(lib().fp8q_kv4_attention_workspace_size(cache._ref, *sizes))
 
 
 def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tensor, kv_len: torch.Tensor,
@@ -617,6 +628,7 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tenso
             _binding.attention(cache._at, dev, q, page_table, kv_len, q_start, max_q_len, float(sm_scale), bool(causal),
                                window, out, lse, workspace) == OK:
         return out
+    max_q_len, window, sm_scale = _whole(max_q_len, "max_q_len"), _whole(window, "window"), float(sm_scale)
     qt, qh = _heads(q, "q", dev, shape)
     T, Hq, D = shape
     if D != cache.head_dim:

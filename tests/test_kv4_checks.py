@@ -433,3 +433,27 @@ def test_offsets_stay_inside_63_bits(L, T, t, h, want):
     assert append(L, c, T=T, kt=t, kh=h, vt=256) == want and append(L, c, T=T, vt=t, vh=h, kt=256) == want
     assert read(L, c, T=T, kt=t, kh=h, vt=256) == want and read(L, c, T=T, vt=t, vh=h, kt=256) == want
     assert attend(L, c, T=T, Hq=2, ot=t, oh=h, qt=0) == want and attend(L, c, T=T, Hq=2, qt=t, qh=h, ot=256) == want
+
+
+# ------------------------------------------------------------ whole numbers ---
+
+def test_binding_whole_numbers(lib, monkeypatch):
+    """Numbers past 64 bits are refused, not cut to what is left of them (a window of 2^64 + 5 to one of 5); numpy's whole
+    numbers are taken, others are not."""
+    seen = []
+    monkeypatch.setattr(fq, "_call", lambda dev, name, *args: seen.append(args))
+    base = dict(q=S((7, 8, 128), BF), cache=a_cache(), page_table=S((3, 9), I32), kv_len=S((3,), I32),
+                q_start=S((4,), I32), max_q_len=4, out=S((7, 8, 128), BF), workspace=S((64,), U8))
+    call = lambda **kw: fq.fp8q_kv4_attention(**{**base, **kw})  # noqa: E731
+    for bad in (2 ** 63, 2 ** 64 + 5, -2 ** 63 - 1):
+        for name in ("window", "max_q_len"):
+            with pytest.raises(ValueError, match=name):
+                call(**{name: bad})
+        with pytest.raises(ValueError):
+            fq.fp8q_kv4_page_bytes(bad, 8, 128)
+    with pytest.raises(TypeError):
+        call(window=5.0)
+    assert not seen
+    call(window=np.int64(2 ** 63 - 1), max_q_len=np.int32(4), sm_scale=np.float32(0.125))
+    assert 2 ** 63 - 1 in seen[0]
+    assert all(not isinstance(a, np.generic) for a in seen[0])
