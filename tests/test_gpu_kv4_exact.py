@@ -1,4 +1,5 @@
-"""Attention over the 4-bit KV cache at long contexts and few parts too many, against 64-bit sums on the device."""
+"""The 4-bit KV cache's operators where parts of long contexts meet, where weights and scores are very small or large,
+and beside strided outputs: against 64-bit sums on the device."""
 import math
 
 import numpy as np
@@ -156,3 +157,36 @@ def test_sequences_that_are_all_empty_need_no_page(rows, q_start):
                               workspace=ws)
         assert bool((out[:-1] == 0).all()) and bool((out[-1] == 7.0).all())
         assert bool((lse[:-1] == -math.inf).all()) and bool((lse[-1] == 7.0).all())
+
+
+def inside(T, H, D):
+    """A buffer of fives, views of it [T, H, D] (token-major, head-major), and whether all outside a view is as it was."""
+    for shape, cut in (((T + 2, H + 3, D + 8), lambda x: x[1:T + 1, 2:H + 2, :D]),
+                       ((H + 2, T + 3, D + 16), lambda x: x[1:H + 1, 2:T + 2, 8:D + 8].transpose(0, 1))):
+        base = torch.full(shape, 5.0, dtype=torch.bfloat16, device=DEV)
+        untouched = torch.ones(shape, dtype=torch.bool, device=DEV)
+        cut(untouched).fill_(False)
+        yield cut(base), lambda: bool((base[untouched] == 5.0).all())
+
+
+@pytest.mark.parametrize("rows,Hq,H,D", [([3, 66], 8, 2, 128), ([1, 2], 8, 2, 128), ([1, 2], 6, 2, 64), ([90, 7], 4, 4, 64)])
+def test_attention_writes_nothing_beside_a_strided_output(rows, Hq, H, D):
+    b = Batch([70, 410], rows, Hq, H, D, 16, seed=41)
+    want, _ = b.call()
+    for out, untouched in inside(sum(rows), Hq, D):
+        b.call(out=out)
+        assert torch.equal(out, want) and untouched()
+
+
+@pytest.mark.parametrize("D,R", [(128, 128), (128, 64), (64, 6), (64, 24)])
+def test_rotation_and_read_back_write_nothing_beside_a_strided_output(D, R):
+    T, H = 37, 3
+    x = torch.randn((T, H, D), device=DEV).to(torch.bfloat16)
+    positions, freq = torch.arange(T, device=DEV), fq.fp8q_rope_frequencies(R)
+    cache, slots = fq.KV4Cache.empty(4, H, 16, D, 0.004, 0.004), torch.arange(T, device=DEV)
+    fq.fp8q_kv4_append(cache, x, x, slots)
+    want, (k, v) = fq.fp8q_rope(x, positions, freq), fq.fp8q_kv4_read(cache, slots)
+    for (out, untouched), (other, as_well) in zip(inside(T, H, D), inside(T, H, D)):
+        assert torch.equal(fq.fp8q_rope(x, positions, freq, out=out), want) and untouched()
+        fq.fp8q_kv4_read(cache, slots, out=(out, other))
+        assert torch.equal(out, k) and torch.equal(other, v) and untouched() and as_well()
