@@ -71,11 +71,17 @@ constexpr int64_t kOneItem = static_cast<int64_t>(1) << 40;
 // 2^-21 of the row's largest, and n keys lose at most n 2^-32 of it below that.  Both are rounded so that P never passes
 // 2^15, whatever the size of the scores.
 constexpr float kSlack = 8.0f, kLift = 7.0f;
+__device__ __forceinline__ float rcp_approx(float x) {    // off by 2^-23 of itself at most
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // The negated base that a largest score asks for; infinity where it is minus infinity (no visible key).
 __device__ __forceinline__ float base_above(float top, float qscale) { return __fmaf_rd(-top, qscale, kLift); }
-// The score up to which it is kept.
-__device__ __forceinline__ float base_limit(float nbase, float qscale) {
-  return __fdiv_rd(__fsub_rd(kLift + kSlack, nbase), qscale);
+// The score up to which it is kept, 2^kSlack above that one in the exponent: an approximate quotient will do, as it is taken
+// a little too small.
+__device__ __forceinline__ float base_limit(float top, float qscale) {
+  return __fadd_rd(top, (kSlack - 0.001f) * rcp_approx(qscale));
 }
 
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t (&o)[4]) {
@@ -163,9 +169,9 @@ __device__ __forceinline__ float pow2(int k) { return __uint_as_float(static_cas
 // V^T's operand pairs two keys in a register: the two keys' nibbles are merged
 // into bytes (two logic operations for four values) before they are widened.
 // E2M1 times E4M3 is exact in f16.  Q is scaled by a power of two per row so
-// that its bf16 values are f16 values (down to about 2^-31 of the row's largest;
-// below, they are rounded to multiples of 2^-38 of it at least); P is rounded to
-// f16.
+// that its bf16 values are f16 values (exactly down to 2^-31 of the row's
+// largest; smaller ones are rounded to multiples of at most 2^-38 of it); P is
+// rounded to f16, its base chosen for that (above).
 //
 // The keys of a (sequence, key head) are cut into steps of WARPS * 32; the
 // list of all steps is cut evenly over the CTAs (stream-K, as in the linear's
@@ -623,7 +629,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) attention_kernel(const __gri
             if (now < was) {
               const float f = ex2(now - was);       // 0 from infinity
               nbase[nt][i] = now;
-              limit[nt][i] = base_limit(now, qscale[nt][i]);
+              limit[nt][i] = base_limit(top[i], qscale[nt][i]);
               l[nt][i] *= f;
 #pragma unroll
               for (int d = 0; d < kSteps; ++d) {

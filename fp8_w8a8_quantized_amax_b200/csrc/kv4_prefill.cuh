@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             if (now < was) {
               f = ex2(now - was);                    // 0 from infinity
               nbase = now;
-              limit = base_limit(now, qscale);
+              limit = base_limit(top, qscale);
               sum *= f;
             }
             if (j > 0) {                             // S of this step was issued after O's last product: O is at rest
