@@ -504,7 +504,7 @@ def fp8q_rope_frequencies(rot_dim: int, theta: float = 500000.0, scaling: Option
 def fp8q_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, interleaved: bool = False,
               inverse: bool = False, mscale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotate bf16 heads x [T, H, D] by positions [T] (int64) times freq (fp64 [rot_dim / 2], from
-    fp8q_rope_frequencies); elements from rot_dim on are copied.  `out` may be x itself."""
+    fp8q_rope_frequencies); elements from rot_dim on are copied.  `out` may be x itself, else must not overlap it."""
     flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
     if out is None:
         out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
@@ -618,9 +618,13 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tenso
 
     q bf16 [T, q_heads, head_dim]; page_table int32 [B, max_pages]; kv_len int32 [B], tokens in the cache.
     q_start int32 [B + 1]: sequence b's rows of q are its last q_start[b + 1] - q_start[b] tokens, at most max_q_len
-    (None: one row per sequence).  Rows behind q_start[B] are left as they were.  lse: fp32 [T, q_heads], written
-    when given.  `workspace`: a zero-filled uint8 buffer of fp8q_kv4_attention_workspace_size bytes (allocated here
-    when None; left zero).  -> out bf16 [T, q_heads, head_dim]"""
+    (None: one row per sequence).  Rows behind the last sequence's are left as they were (in a new `out` they hold
+    anything).  lse: fp32 [T, q_heads], written when given.  `workspace`: a uint8 buffer of
+    fp8q_kv4_attention_workspace_size bytes, zero-filled before its first use and then kept from call to call (allocated
+    here when None, which costs its zero-filling each time: up to 39 MB for many rows), not shared by calls in flight at
+    once.  `out` must not overlap q.
+    max_q_len chooses the kernel for the whole call: prompts and single tokens are faster in two calls.
+    -> out bf16 [T, q_heads, head_dim]"""
     dev, shape = cache._dev, q.shape
     if sm_scale is None:
         sm_scale = cache.head_dim ** -0.5
@@ -660,7 +664,8 @@ def fp8q_kv4_attention(q: torch.Tensor, cache: KV4Cache, page_table: torch.Tenso
 
 
 def device_error(clear: bool = True) -> int:
-    """Device-side error word (nonzero after a kernel gave up waiting)."""
+    """Device-side error word: nonzero after a kernel gave up waiting, or after the KV cache's calls met a slot past the
+    cache (0x201), a page outside it (0x202) or bad lengths of a sequence (0x203)."""
     return int(lib().fp8q_device_error(1 if clear else 0))
 
 

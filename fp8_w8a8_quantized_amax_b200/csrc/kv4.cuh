@@ -3,8 +3,8 @@
 // For each (page, head) K and V hold one slab each: page_size rows of D/2 code
 // bytes (E2M1, the even element in the low nibble), then page_size rows of
 // D/16 scale bytes (E4M3, one per 16 elements).  A slab is one contiguous run
-// of 9 D / 16 bytes a token, a multiple of 16 bytes for every page size, so
-// that attention can fetch it with bulk copies.  A value is
+// of 9 D / 16 bytes a token; it, its scales and every 16 rows of either are
+// multiples of 16 bytes, so that 16-byte copies and loads stay aligned.  A value is
 //   E2M1(code) * E4M3(scale) * g,
 // g one static fp32 per tensor.  E2M1 has two significant bits and E4M3 four,
 // so code times scale is exact in f16 (and in bf16): what reads the cache
@@ -112,9 +112,11 @@ __device__ __forceinline__ uint32_t encode2(float nx0, float nx1, uint64_t ny2, 
 // its definition gives, a whole E2M1 step away.  A block's partners (half
 // layout) are read from memory as well; they are another thread's elements, so
 // they come from L1.  8192 tokens of 8 heads of 128, four tokens a CTA: 21 us,
-// 2.0 TB/s; 65% of the issue slots are taken (quotients, conversions and the
-// fp64 rotation), which loads one step further ahead and fewer CTAs did not
-// change.  64 tokens: 2.4 us.
+// 2.0 TB/s (D = 64: 12 us; 4 bytes spill there); 65% of the issue slots are taken
+// (quotients, conversions and the fp64 rotation), no unit is at its limit, and
+// loads one step further ahead and fewer CTAs changed nothing.  64 tokens: 2.4 us.
+// A CTA has 2 tokens heads D / 16 blocks for its 256 threads, whatever the number
+// of heads: 8192 tokens of one head take 10 us, of two 11.
 template <int D>
 __global__ void __launch_bounds__(256, 4) append_kernel(const __grid_constant__ AppendParams p, int tokens) {
   constexpr int kBlocks = D / 16, kCols = D / 32;

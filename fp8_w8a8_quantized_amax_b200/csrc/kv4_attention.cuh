@@ -180,14 +180,15 @@ __device__ __forceinline__ float pow2(int k) { return __uint_as_float(static_cas
 // maximum, sum and O^T; the warps' results are joined where an item ends.  An
 // item cut between CTAs is joined by the last of them to finish, in CTA order.
 //
-// Measured: 64 sequences of 410 .. 8192 keys, 32 + 8 heads of 128, one token
-// each: 76 us, 4.3 TB/s of cache (0.67 of a copy).  HBM is not what bounds it
-// there: a key's conversions, products with the scales and matrix instructions
-// keep the issue slots 62% and the ALUs 50% busy.  One token behind 131072 keys
-// (three heads to a key head): 41 us, of which the joins take about 8.  One
-// sequence of 500 keys: 8.6 us, the latency of a prologue, four steps and a join.
-// 16 sequences of four drafted tokens, 32 rows and 4096 keys: 48 us, bound like
-// the first by the instructions of two tiles of 16 rows.
+// Measured, launches back to back: 64 sequences of 410 .. 8192 keys, 32 + 8 heads
+// of 128, one token each: 76 us, 4.3 TB/s of cache (0.67 of a copy).  HBM does not
+// bound it there, nor does any unit: the issue slots are 62% and the ALUs 50%
+// busy with a key's conversions, products with the scales and matrix
+// instructions, whose latencies 16 warps an SM do not hide.  One token behind
+// 131072 keys (three heads to a key head): 42 us, of which the joins take about
+// 8.  One sequence of 500 keys: 8.6 us, the latency of a prologue, four steps and
+// a join.  16 sequences of four drafted tokens, 32 rows and 4096 keys: 48 us; two
+// tiles of 16 rows widen every key twice, with 12 warps an SM.
 namespace few {
 
 constexpr int kTile = 32;     // keys of a warp per step

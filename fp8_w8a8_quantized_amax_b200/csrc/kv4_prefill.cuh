@@ -22,12 +22,15 @@
 // itself; its parts are joined by the last of its CTAs, in CTA order.
 //
 // Measured: 2048 new tokens of 32 heads behind 6144 cached ones (8 key heads, D =
-// 128): 240 us, 1.0 PFLOP/s of the visible products (0.61 of what a library
-// product reaches).  A step of 256 rows takes 3.9 K cycles where its products
-// take 2.05 K: a tile's chain S, maximum, exponentials, P . V is longer than the
-// other tile's share of the tensor cores, and a row's two passes over tensor
-// memory by one thread are its longest link.  Sixteen softmax warps (one pass, S
-// held in registers) spilled and were slower.
+// 128): 262 to 267 us a call on new inputs, 0.92 PFLOP/s of the visible products
+// (0.56 of what a library product reaches); 245 us for launches back to back.  A
+// step of 256 rows takes 3.9 K cycles where its products take 2.05 K: a tile's
+// chain S, maximum, exponentials, P . V is longer than the other tile's share of
+// the tensor cores, and a row's two passes over tensor memory by one thread are
+// its longest link.  13 warps compiled together leave 128 registers a thread: at D
+// = 128 the roles spill (128 bytes stored, 496 loaded), at D = 64 hardly (8, 40).
+// Sixteen softmax warps (one pass, S held in registers) spilled and were slower;
+// eight with registers moved to them have not been tried.
 #pragma once
 
 #include "kv4_attention.cuh"

@@ -70,7 +70,10 @@ struct Params {
 };
 
 // Any strides and alignment, any even R: one thread per pair of a (token, head);
-// the dimensions behind the rotated part are copied by the same threads.
+// the dimensions behind the rotated part are copied by the same threads.  An
+// angle in fp64 for each pair and 2-byte accesses bound it: 8192 tokens of 40
+// heads of 128 take 57 us with R = 24 (2.9 TB/s), 73 with R = 40, 147 with R = 128
+// and unaligned rows, where the kernel below takes 28 to 35.
 __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ Params p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -104,8 +107,9 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ P
 // list, one at a time: the loads in flight come from eight CTAs an SM (32
 // registers; the interleaved layout needs a few more, so six: 3.5 against 3.8
 // us for 777 tokens of 13 heads of 64), which beat two units a thread with four
-// CTAs and loads one step ahead.  8192 tokens of 8 + 32 heads of 128 take 28.5
-// us, 5.9 TB/s (four tokens a CTA; 33.8 us with eight).
+// CTAs and loads one step ahead (8 and 24 bytes spill).  8192 tokens of 8 + 32 heads
+// of 128 take 28.5 us, 5.9 TB/s (four tokens a CTA; 33.8 us with eight); interleaved
+// 32.8, and 34.6 with R = 64.
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(256, INTERLEAVED ? 6 : 8) rope_vec_kernel(const __grid_constant__ Params p, int tokens) {
   // [tokens][4][U][2] (cos, sin): pairs 2j and 2j + 1 of neighbouring units side by side, so that lanes read other banks

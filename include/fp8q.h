@@ -267,7 +267,9 @@ FP8Q_API size_t fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int m
 FP8Q_API const char* fp8q_status_string(int status);
 
 /* Reads the device-side error word of the current device: 0 when no kernel
- * has given up waiting, otherwise a nonzero code naming the wait site.  It
+ * has given up waiting or met a bad index, otherwise a nonzero code naming the
+ * wait site, or 0x201 (a slot past the cache), 0x202 (a page outside it) or 0x203
+ * (a sequence's lengths), set by the KV cache's entry points.  It
  * synchronizes the device.  clear != 0 resets the word to 0 afterwards and,
  * when it was nonzero, also zeroes fp8_linear_noalloc's in-library scratch on
  * this device.  Returns -1 when a CUDA call fails. */
@@ -446,7 +448,9 @@ FP8Q_API fp8q_status fp8q_kv4_read(const fp8q_kv4_cache* cache, const int64_t* s
  *                   largest at 2^7 .. 2^15: one below 2^-21 of it keeps fewer than 11 bits.
  *   max_q_len       the largest number of rows of a sequence; longer ones set the
  *                   device error word.  Lengths stay on the device: a captured call
- *                   can be replayed with other lengths up to these bounds.
+ *                   can be replayed with other lengths up to these bounds.  It chooses
+ *                   the kernel for all sequences of the call: prompts and single tokens
+ *                   are faster in two calls (each with its part of Q and O).
  *   lse             [T, Hq] fp32, written when not NULL: log sum_j exp(sm_scale q.k_j).
  *   workspace       fp8q_kv4_attention_workspace_size bytes, 16-byte aligned.  Its first
  *                   FP8Q_KV4_WORKSPACE_HEADER bytes are zero before its first use and left
